@@ -17,7 +17,9 @@ __all__ = ["GdnError", "lib", "gdn_decode_step", "gdn_decode_step_commit", "gdn_
            "gdn_prefill_two_pass", "gdn_prefill_two_pass_workspace_bytes", "gdn_prefill_two_pass_noalloc",
            "NOALLOC_SCRATCH_BYTES", "conv_decode",
            "slot_commit",
-           "slot_reset", "slot_copy", "check_slots", "traffic_probe", "status_string", "LIB_PATH", "EXPORTS"]
+           "slot_reset", "slot_copy", "check_slots", "traffic_probe", "status_string", "LIB_PATH", "EXPORTS",
+           "rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "kv_page_workspace_bytes",
+           "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -104,6 +106,7 @@ def lib() -> ctypes.CDLL:
     L.gdn_slot_copy.argtypes = [ctypes.POINTER(Dims), P, P, P, P, i32, P]
     L.gdn_traffic_probe.restype = i32
     L.gdn_traffic_probe.argtypes = [ctypes.POINTER(Probe), i32, i32, i32, i32, i32, P, P, P, P, P]
+    _attention.declare(L)
     _lib = L
     return L
 
@@ -536,3 +539,13 @@ def traffic_probe(state, read_slot, write_slot, sink, *, traffic: str = "copy", 
         _check("gdn_traffic_probe", lib().gdn_traffic_probe(
             ctypes.byref(pr), n, H, d_k, d_v, N, _ptr(state), _ptr(read_slot), _ptr(write_slot), _ptr(sink),
             _stream(stream, dev)))
+
+
+# ------------------------------------------------------------------ the full-attention layers
+
+from . import attention as _attention  # noqa: E402  (it takes this module's helpers)
+from .attention import (attn_paged, attn_paged_workspace_bytes, attn_prologue, kv_page_compact,  # noqa: E402
+                        kv_page_copy, kv_page_fork, kv_page_free, kv_page_reserve, kv_page_workspace_bytes,
+                        rope_freqs)
+
+EXPORTS += _attention.EXPORTS

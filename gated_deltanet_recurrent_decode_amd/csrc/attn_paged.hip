@@ -1,0 +1,587 @@
+// attn_paged.hip -- attention of new tokens over a paged KV cache (gfx950).
+//
+// o = sum_j softmax_j(scale q.k_j) v_j, in one pass over the keys with a running
+// maximum m and sum l: for each block of keys, m' = max(m, s), l = l e^(m - m')
+// + sum e^(s - m'), o = o e^(m - m') + sum e^(s - m') v; at the end o / l.
+//
+// The query heads of a group share their kv head, so a sequence's (token, head
+// of the group) pairs form the rows of a tile of 16 and each key is read once
+// for all of them.  Both products run on the matrix cores transposed, S^T = K
+// Q^T and O^T = V^T P^T (16 x 16 x 32 bf16), which makes the layouts meet with
+// no exchange between lanes: lane (g, n) of S^T holds row n's scores of keys
+// 4g..4g+3 of two 16-key tiles, which is a P^T operand as it stands once the
+// contraction's 32 places are dealt out to the keys in that order, and the V^T
+// operand wants, of those same eight keys, one column of v, which a lane makes
+// from eight 16-byte pieces of their rows by one byte permute a dword.  So K and
+// V go from memory to registers to the matrix cores: no LDS and no barrier on
+// the way.
+//
+// Work is dealt out by the key, not by the sequence: the units of 128 keys of all
+// (sequence, kv head, tile) triples lie on one line, cut into equal pieces, one a
+// workgroup.  A workgroup finds its piece from the lengths on the device (a
+// captured step follows its lengths) and finishes what lies whole in it; of a
+// triple that is cut it leaves (o, m, l) in the workspace for the second kernel.
+
+#include "attn_common.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int TM = 16;    // rows of a tile
+constexpr int UNIT = 128; // keys of a unit: a block of 32 a wave
+constexpr int NT = 256;
+
+enum { kSkip = -1, kNormal = 0, kZero = 1, kNan = 2 };
+
+struct Seq {
+    int kind, first, n, L, lo; // first token, tokens, keys, first key in reach of the window
+    int r;                     // row of the table
+    int tiles, units;          // tiles of rows, units of a tile
+};
+
+__device__ __forceinline__ Seq read_seq(const AttnParams &p, int b)
+{
+    Seq s;
+    s.first = p.cu[b];
+    const int e = p.cu[b + 1];
+    s.n = e - s.first;
+    s.kind = kNormal;
+    s.r = p.row[b];
+    s.L = s.lo = 0;
+    s.tiles = s.units = 0;
+    if (s.first < 0 || e > p.T || e <= s.first) {
+        s.kind = kSkip;
+        return s;
+    }
+    if (s.r == 0) {
+        s.kind = kZero;
+    } else if (s.r < 0 || s.r >= p.R || s.n > p.max_new) {
+        s.kind = kNan;
+    } else {
+        s.L = p.kv_len[s.r];
+        if (s.L < 0 || s.L > (p.width << p.page_shift)) {
+            s.kind = kNan;
+            s.L = 0;
+        } else if (p.window > 0 && s.L - s.n - p.window + 1 > 0) {
+            s.lo = (s.L - s.n - p.window + 1) & ~31;
+        }
+    }
+    s.tiles = (int)(((int64_t)s.n * p.G + TM - 1) / TM);
+    const int span = s.L - s.lo;
+    s.units = span > UNIT ? (span + UNIT - 1) / UNIT : 1;
+    return s;
+}
+
+__device__ __forceinline__ long long seq_units(const AttnParams &p, const Seq &s)
+{
+    return (long long)p.H_kv * s.tiles * s.units;
+}
+
+struct Place {
+    int b;          // sequence
+    long long before; // units before it
+    long long total;  // units of the call
+};
+
+// Where the line of units holds what `hit` asks for (a predicate of a sequence,
+// its first unit and the units of the call), and the units of the call.  b = -1 if nowhere.
+template <class Hit>
+__device__ Place locate(const AttnParams &p, Hit hit)
+{
+    __shared__ long long wave_sum[4];
+    __shared__ long long found_before;
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    long long total = 0;
+    if (tid == 0)
+        found = -1;
+    for (int pass = 0; pass < 2; ++pass) {
+        long long run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += NT) {
+            const int b = b0 + tid;
+            Seq s;
+            long long u = 0;
+            if (b < p.B) {
+                s = read_seq(p, b);
+                u = seq_units(p, s);
+            }
+            long long inc = u;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const long long o = __shfl_up(inc, m);
+                if (lane >= m)
+                    inc += o;
+            }
+            __syncthreads();
+            if (lane == 63)
+                wave_sum[wave] = inc;
+            __syncthreads();
+            long long before = run;
+            for (int w = 0; w < 4; ++w) {
+                if (w < wave)
+                    before += wave_sum[w];
+                run += wave_sum[w];
+            }
+            if (pass == 1 || p.B <= NT) {
+                if (u > 0 && hit(s, before + inc - u, u, p.B <= NT ? run : total)) {
+                    found = b;
+                    found_before = before + inc - u;
+                }
+            }
+        }
+        if (pass == 0)
+            total = run;
+        if (p.B <= NT)
+            break;
+    }
+    __syncthreads();
+    Place at;
+    at.b = found;
+    at.before = found_before;
+    at.total = total;
+    return at;
+}
+
+// Pieces of the line, one a workgroup, none of them empty; piece w begins at unit piece(w).
+__device__ __forceinline__ int pieces_of(const AttnParams &p, long long total)
+{
+    return total < p.workgroups ? (int)total : p.workgroups;
+}
+
+__device__ __forceinline__ long long piece(long long total, int w, int pieces) { return total * w / pieces; }
+
+// The piece that holds unit u: the last w with piece(w) <= u.
+__device__ __forceinline__ int owner_of(long long total, long long u, int pieces)
+{
+    return (int)(((u + 1) * pieces - 1) / total);
+}
+
+// log2 of a sum relative to a maximum, as a natural logarithm
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+} // namespace
+
+// D = 64, 128 or 256.  A lane owns EV consecutive columns of v in each of NH
+// 128-column parts (D = 64: four columns of one part).
+template <int D, bool E4M3>
+__global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
+{
+    constexpr int EV = D == 64 ? 4 : 8, NH = D / (16 * EV), NS = D / 32;
+    constexpr int LD = D + 4; // LDS row, padded against bank conflicts
+    __shared__ __align__(16) float sm_o[4][TM][LD];
+    __shared__ float sm_m[4][TM], sm_l[4][TM], sm_mm[TM], sm_ll[TM];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int n_ = lane & 15, g = lane >> 4;
+    const int w = blockIdx.x;
+
+    const Place at = locate(p, [&](const Seq &, long long before, long long units, long long total) {
+        const int pieces = pieces_of(p, total);
+        const long long u0 = piece(total, w, pieces);
+        return w < pieces && before <= u0 && u0 < before + units;
+    });
+    if (at.b < 0)
+        return;
+    const int pieces = pieces_of(p, at.total);
+    long long u = piece(at.total, w, pieces);
+    const long long u_end = piece(at.total, w + 1, pieces);
+    const long long u_begin = u;
+    int b = at.b;
+    long long before = at.before;
+
+    while (u < u_end) {
+        const Seq s = read_seq(p, b);
+        const long long units = seq_units(p, s);
+        if (u >= before + units) {
+            before += units;
+            ++b;
+            continue;
+        }
+        const long long v = u - before;
+        const long long ht = v / s.units;
+        const int unit0 = (int)(v - ht * s.units);
+        const int tile = (int)(ht % s.tiles), h = (int)(ht / s.tiles);
+        const long long t0 = before + ht * s.units, t1 = t0 + s.units;
+        const long long e = t1 < u_end ? t1 : u_end;
+        const int unit1 = unit0 + (int)(e - u);
+        const bool whole = u == t0 && e == t1;
+        const int slot = u == u_begin ? 0 : 1;
+        u = e;
+
+        // this lane's row: a token and a head of the group
+        const int row = tile * TM + n_, rows = s.n * p.G;
+        const bool valid = row < rows && s.kind == kNormal;
+        const int tok = row / p.G, head = h * p.G + row % p.G;
+        const int pos = valid ? s.L - s.n + tok : -1;
+        const int low = p.window > 0 ? pos - p.window + 1 : 0;
+        const int last_row = (rows < (tile + 1) * TM ? rows : (tile + 1) * TM) - 1;
+        const int min_pos = s.L - s.n + tile * TM / p.G, max_pos = s.L - s.n + last_row / p.G;
+
+        bf16x8 qf[NS];
+        const uint16_t *qp = p.q.p + (int64_t)(s.first + tok) * p.q.row + (int64_t)head * p.q.head;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            // the 8-bit cache is read 16 values at a time, two steps of the contraction
+            const int d0 = E4M3 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
+            u32x4 x = {0u, 0u, 0u, 0u};
+            if (valid)
+                x = *reinterpret_cast<const u32x4 *>(qp + d0);
+            qf[i] = __builtin_bit_cast(bf16x8, x);
+        }
+
+        float m = neg_inf(), l = 0.f;
+        f32x4 acc[NH][EV];
+#pragma unroll
+        for (int a = 0; a < NH; ++a)
+#pragma unroll
+            for (int c = 0; c < EV; ++c)
+                acc[a][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        bool bad = false;
+        const float scale = E4M3 ? p.scale * p.k_scale[h] : p.scale;
+
+        const int k_end = s.lo + unit1 * UNIT < s.L ? s.lo + unit1 * UNIT : s.L;
+        for (int key0 = s.lo + unit0 * UNIT + wave * 32; key0 < k_end; key0 += UNIT) {
+            if (key0 > max_pos || (p.window > 0 && key0 + 31 <= min_pos - p.window))
+                continue; // no row of the tile sees the block
+            int page[2];
+            const int32_t *tab = p.page_table + (int64_t)s.r * p.width;
+            page[0] = tab[key0 >> p.page_shift];
+            page[1] = key0 + 16 < s.L ? tab[(key0 + 16) >> p.page_shift] : 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (page[t] < 1 || page[t] >= p.N) { // uniform
+                    const int k0 = key0 + 16 * t;
+                    bad |= k0 < s.L && pos >= k0 && low <= k0 + 15;
+                    page[t] = 0;
+                }
+            }
+            // cells of the two 16-key tiles
+            int64_t cell[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                cell[t] = ((((int64_t)page[t] * p.H_kv + h) << p.page_shift) +
+                           ((key0 + 16 * t) & ((1 << p.page_shift) - 1))) * D;
+
+            f32x4 sc[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if constexpr (E4M3) {
+                    const uint8_t *kp = static_cast<const uint8_t *>(p.k_pages) + cell[t] + n_ * D + g * 16;
+#pragma unroll
+                    for (int i = 0; i < NS / 2; ++i) {
+                        const u32x4 x = *reinterpret_cast<const u32x4 *>(kp + i * 64);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const u32x4 y = {e4m3_to_bf16<false>(x[2 * q]), e4m3_to_bf16<true>(x[2 * q]),
+                                             e4m3_to_bf16<false>(x[2 * q + 1]), e4m3_to_bf16<true>(x[2 * q + 1])};
+                            sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, y),
+                                                                            qf[2 * i + q], sc[t], 0, 0, 0);
+                        }
+                    }
+                } else {
+                    const uint16_t *kp = static_cast<const uint16_t *>(p.k_pages) + cell[t] + n_ * D + g * 8;
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        const u32x4 x = *reinterpret_cast<const u32x4 *>(kp + i * 32);
+                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), qf[i], sc[t], 0,
+                                                                        0, 0);
+                    }
+                }
+            }
+
+            // v: eight keys of this lane (4g.. of both tiles), EV columns of each part, as bf16 pairs
+            uint32_t vr[NH][8][EV / 2];
+#pragma unroll
+            for (int a = 0; a < NH; ++a)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t o = cell[j >> 2] + (g * 4 + (j & 3)) * D + a * 128 + n_ * EV;
+                    if constexpr (E4M3) {
+                        const uint8_t *vp = static_cast<const uint8_t *>(p.v_pages) + o;
+#pragma unroll
+                        for (int c = 0; c < EV / 4; ++c) {
+                            const uint32_t x = reinterpret_cast<const uint32_t *>(vp)[c];
+                            vr[a][j][2 * c] = e4m3_to_bf16<false>(x);
+                            vr[a][j][2 * c + 1] = e4m3_to_bf16<true>(x);
+                        }
+                    } else {
+                        const uint16_t *vp = static_cast<const uint16_t *>(p.v_pages) + o;
+#pragma unroll
+                        for (int c = 0; c < EV / 2; ++c)
+                            vr[a][j][c] = reinterpret_cast<const uint32_t *>(vp)[c];
+                    }
+                }
+
+            // masks, where some row of the tile does not see every key of the block
+            const bool mixed = key0 + 31 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
+            float pr[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                pr[j] = sc[j >> 2][j & 3] * scale;
+            bool odd_any = false;
+            if (mixed) {
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int key = key0 + (j >> 2) * 16 + g * 4 + (j & 3);
+                    if (key > pos || key < low)
+                        pr[j] = neg_inf();
+                    const bool past = key >= s.L;
+#pragma unroll
+                    for (int a = 0; a < NH; ++a)
+#pragma unroll
+                        for (int c = 0; c < EV / 2; ++c) {
+                            const uint32_t x = past ? 0u : vr[a][j][c];
+                            vr[a][j][c] = x;
+                            odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+                        }
+                }
+                // An infinity or NaN in v must not reach rows that do not see its key (0 times it is
+                // NaN): such values leave the product here and are added to the rows that do below.
+                odd_any = __ballot(odd) != 0;
+                if (odd_any) {
+#pragma unroll
+                    for (int a = 0; a < NH; ++a)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int c = 0; c < EV / 2; ++c) {
+                                uint32_t x = vr[a][j][c];
+                                if ((x & 0x7f80u) == 0x7f80u)
+                                    x &= 0xffff0000u;
+                                if ((x & 0x7f800000u) == 0x7f800000u)
+                                    x &= 0xffffu;
+                                vr[a][j][c] = x;
+                            }
+                }
+            }
+
+            float top = pr[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                top = fmaxf(top, pr[j]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m_new = fmaxf(m, top);
+            const float m_safe = m_new == neg_inf() ? 0.f : m_new;
+            const float keep = __builtin_amdgcn_exp2f(m - m_safe);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                pr[j] = __builtin_amdgcn_exp2f(pr[j] - m_safe);
+                sum += pr[j];
+            }
+            l = fmaf(l, keep, sum); // this lane's keys only; joined at the end
+            m = m_new;
+            // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and o is rounded to
+            // bf16 in the end
+            const u32x4 pb = {pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3]), pack_bf16(pr[4], pr[5]),
+                              pack_bf16(pr[6], pr[7])};
+#pragma unroll
+            for (int a = 0; a < NH; ++a)
+#pragma unroll
+                for (int c = 0; c < EV; ++c) {
+                    constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;
+                    const uint32_t sel = (c & 1) ? kHigh : kLow;
+                    u32x4 x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = __builtin_amdgcn_perm(vr[a][2 * j + 1][c >> 1], vr[a][2 * j][c >> 1], sel);
+                    acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
+                                                                        __builtin_bit_cast(bf16x8, pb),
+                                                                        acc[a][c] * keep, 0, 0, 0);
+                }
+            if (odd_any) {
+                for (int key = key0; key < key0 + 32 && key < s.L; ++key) {
+                    const bool sees = key <= pos && key >= low;
+                    const int64_t o = cell[(key - key0) >> 4] + ((key - key0) & 15) * D;
+#pragma unroll
+                    for (int a = 0; a < NH; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int c = 0; c < EV; ++c) {
+                                const int64_t q = o + a * 128 + (g * 4 + i) * EV + c;
+                                uint32_t x;
+                                if constexpr (E4M3)
+                                    x = e4m3_to_bf16<false>(static_cast<const uint8_t *>(p.v_pages)[q]) << 16;
+                                else
+                                    x = (uint32_t) static_cast<const uint16_t *>(p.v_pages)[q] << 16;
+                                if (sees && (x & 0x7f800000u) == 0x7f800000u)
+                                    acc[a][c][i] += __uint_as_float(x);
+                            }
+                }
+            }
+        }
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        // a needed page outside the pool, or a sequence that cannot be used
+        if (__shfl_xor((int)bad, 16) | (int)bad)
+            bad = true;
+        if (__shfl_xor((int)bad, 32) | (int)bad)
+            bad = true;
+        if (bad || s.kind == kNan)
+            l = quiet_nan();
+
+        // the four waves' keys together
+        __syncthreads(); // the LDS of the piece before is free
+        if (g == 0) {
+            sm_m[wave][n_] = m;
+            sm_l[wave][n_] = l;
+        }
+        __syncthreads();
+        float mm = neg_inf();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            mm = fmaxf(mm, sm_m[q][n_]);
+        const float mm_safe = mm == neg_inf() ? 0.f : mm;
+        const float mine = __builtin_amdgcn_exp2f(m - mm_safe);
+#pragma unroll
+        for (int a = 0; a < NH; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < EV; c += 4)
+                    *reinterpret_cast<f32x4 *>(&sm_o[wave][n_][a * 128 + (g * 4 + i) * EV + c]) =
+                        f32x4{acc[a][c][i], acc[a][c + 1][i], acc[a][c + 2][i], acc[a][c + 3][i]} * mine;
+        if (wave == 0 && g == 0) {
+            float ll = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                ll += sm_l[q][n_] * __builtin_amdgcn_exp2f(sm_m[q][n_] - mm_safe);
+            sm_mm[n_] = mm;
+            sm_ll[n_] = ll;
+        }
+        __syncthreads();
+        constexpr int C4 = D / 4;
+        for (int x = tid; x < TM * C4; x += NT) {
+            const int rr = x / C4, c = (x % C4) * 4;
+            const int ro = tile * TM + rr;
+            if (ro >= rows)
+                break;
+            f32x4 o = *reinterpret_cast<const f32x4 *>(&sm_o[0][rr][c]);
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                o += *reinterpret_cast<const f32x4 *>(&sm_o[q][rr][c]);
+            const float ll = sm_ll[rr];
+            const int64_t tk = s.first + ro / p.G;
+            const int hq = h * p.G + ro % p.G;
+            if (whole) {
+                const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+                const float inv = ll == 0.f ? 0.f : vs / ll;
+                const u32x2 y = {pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+                *reinterpret_cast<u32x2 *>(p.out.p + tk * p.out.row + (int64_t)hq * p.out.head + c) = y;
+                if (c == 0 && p.lse)
+                    p.lse[tk * p.H_q + hq] = lse_of(sm_mm[rr], ll);
+            } else {
+                const int64_t part = ((int64_t)w * 2 + slot) * TM + rr;
+                *reinterpret_cast<f32x4 *>(p.part_o + part * D + c) = o;
+                if (c == 0) {
+                    p.part_ml[part * 2] = sm_mm[rr];
+                    p.part_ml[part * 2 + 1] = ll;
+                }
+            }
+        }
+    }
+}
+
+// The rows whose keys were cut into pieces: their parts' (o, m, l) together, in
+// the order of the pieces.  A workgroup a token and kv head, a wave a row.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams p)
+{
+    constexpr int E = D / 64;
+    const int t = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Place at = locate(p, [&](const Seq &s, long long, long long, long long) {
+        return t >= s.first && t < s.first + s.n;
+    });
+    if (at.b < 0)
+        return;
+    const Seq s = read_seq(p, at.b);
+    const int pieces = pieces_of(p, at.total);
+    for (int q = wave; q < p.G; q += 4) {
+        const int row = (t - s.first) * p.G + q;
+        const int tile = row / TM, rr = row % TM;
+        const long long u0 = at.before + ((long long)h * s.tiles + tile) * s.units, u1 = u0 + s.units;
+        const int w0 = owner_of(at.total, u0, pieces);
+        int w1 = owner_of(at.total, u1 - 1, pieces);
+        w1 = w1 < pieces ? w1 : pieces - 1;
+        if (w0 == w1)
+            continue; // finished where it was computed
+        const int slot0 = piece(at.total, w0, pieces) == u0 ? 0 : 1;
+        float m = neg_inf();
+        for (int w = w0 + lane; w <= w1; w += 64)
+            m = fmaxf(m, p.part_ml[(((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TM + rr) * 2]);
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1)
+            m = fmaxf(m, __shfl_xor(m, x));
+        const float m_safe = m == neg_inf() ? 0.f : m;
+        float l = 0.f, o[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            o[i] = 0.f;
+        for (int w = w0; w <= w1; ++w) {
+            const int64_t part = ((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TM + rr;
+            const float f = __builtin_amdgcn_exp2f(p.part_ml[part * 2] - m_safe);
+            l = fmaf(p.part_ml[part * 2 + 1], f, l);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                o[i] = fmaf(p.part_o[part * D + i * 64 + lane], f, o[i]);
+        }
+        const int hq = h * p.G + q;
+        const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+        const float inv = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            p.out.p[(int64_t)t * p.out.row + (int64_t)hq * p.out.head + i * 64 + lane] = f32_to_bf16_rne(o[i] * inv);
+        if (lane == 0 && p.lse)
+            p.lse[(int64_t)t * p.H_q + hq] = lse_of(m, l);
+    }
+}
+
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t attn_paged_layout(int max_new, int G, int d, void *base, AttnParams *p)
+{
+    (void)max_new;
+    (void)G;
+    const int workgroups = 2 * device_cus();
+    const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4);
+    if (p) {
+        p->workgroups = workgroups;
+        p->part_o = static_cast<float *>(base);
+        p->part_ml = reinterpret_cast<float *>(static_cast<char *>(base) + o);
+    }
+    return o + ml;
+}
+
+template <int D, bool E4M3>
+static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
+{
+    AttnParams q = p;
+    void *args[] = {&q};
+    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_rows_kernel<D, E4M3>),
+                                   dim3((unsigned)p.workgroups), dim3(NT), args, 0, stream);
+    if (e == hipSuccess)
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_join_kernel<D, E4M3>),
+                            dim3((unsigned)p.T, (unsigned)p.H_kv), dim3(NT), args, 0, stream);
+    return e;
+}
+
+hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
+{
+    if (d == 64)
+        return e4m3 ? launch_de<64, true>(p, stream) : launch_de<64, false>(p, stream);
+    if (d == 128)
+        return e4m3 ? launch_de<128, true>(p, stream) : launch_de<128, false>(p, stream);
+    return e4m3 ? launch_de<256, true>(p, stream) : launch_de<256, false>(p, stream);
+}
+
+} // namespace gdn

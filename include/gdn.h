@@ -351,6 +351,230 @@ gdn_status gdn_slot_reset(const gdn_dims *dims, float *state, gdn_bf16 *conv_sta
 gdn_status gdn_slot_copy(const gdn_dims *dims, float *state, gdn_bf16 *conv_state, const int32_t *src_slots,
                          const int32_t *dst_slots, int32_t n, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The full-attention layers of the same hybrid model, over a paged KV cache.
+ *
+ * The pages of a layer's cache are two arrays, k and v, each
+ * [N][H_kv][page_size][d]: cell (p, h, o) is one token's head.  Page 0 is the
+ * null page: no entry point writes it, and a page table entry of 0 means "no
+ * page".  A request is a row of the page table [R][table_width] int32: the
+ * token at position t of row r lives in page page_table[r][t / page_size], at
+ * offset t % page_size.  Row 0 is the null row for padding, as slot 0 is for
+ * the GDN state.  kv_len [R] int32 counts a row's tokens.
+ *
+ * A call takes B sequences with packed new tokens: sequence b owns tokens
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 (n_b of them) of the packed arrays and row
+ * row[b] of the table, whose kv_len already counts them (kv_page_reserve adds
+ * them and their pages), so its token i stands at position
+ * kv_len[row] - n_b + i.  Every n_b may differ: single decoding tokens, drafted
+ * tokens and prompt chunks go in one call.
+ *
+ * gdn_attn_dims
+ *   B  sequences (0: nothing to do);  T  packed new tokens;  R  rows of the
+ *   page table;  H_q, H_kv  heads, H_q a multiple of H_kv: query head h reads
+ *   kv head h / (H_q / H_kv);  d  head dim, 64, 128 or 256;  N  pages with the
+ *   null page;  page_size  16, 32, 64, 128 or 256;  table_width  entries of a
+ *   row;  max_new  no sequence of the call has more new tokens (it picks the
+ *   kernel; a longer one gets NaN outputs);  window  a token sees at most the
+ *   last `window` positions, itself among them, 0: all;  cache_type  what k and
+ *   v hold: 0 bf16, 1 e4m3 (the OCP 8-bit float), a stored 1.0 standing for
+ *   k_scale[h] or v_scale[h]
+ */
+typedef struct gdn_attn_dims {
+    int32_t B, T, R, H_q, H_kv, d, N, page_size, table_width, max_new, window, cache_type;
+} gdn_attn_dims;
+
+/* bf16 heads of packed tokens: head h of token t starts at
+ * data + t*row_stride + h*head_stride (elements); its d values are contiguous.
+ * data 16-byte aligned, strides multiples of 8 (GDN_ERR_UNSUPPORTED otherwise). */
+typedef struct gdn_heads {
+    gdn_bf16 *data;
+    int64_t row_stride, head_stride;
+} gdn_heads;
+
+/* One layer's cache.  k and v 16-byte aligned; the scales [H_kv] fp32 are
+ * required for e4m3 and ignored for bf16. */
+typedef struct gdn_kv_cache {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    const int32_t *page_table; /* [R][table_width] */
+    const int32_t *kv_len;     /* [R] */
+} gdn_kv_cache;
+
+/* Rotary positions.  freqs [rot/2] fp64 on the device, radians a position
+ * (gdn_rope_freqs fills them on the host); rot, even, in [0, d]: the first rot
+ * values of a head turn, the rest pass; pairs are (j, j + rot/2), or with
+ * interleaved (2j, 2j + 1); scale multiplies the turned values (1 unless the
+ * frequencies were stretched). */
+typedef struct gdn_rope {
+    const double *freqs;
+    int32_t rot, interleaved;
+    float scale;
+} gdn_rope;
+
+/* RMS norm of each q and k head before the rotation, in fp32:
+ * y = x / sqrt(mean(x^2) + eps) * (add + weight).  Weights [d] bf16, 16-byte
+ * aligned; NULL leaves the heads as they are.  add = 1 for weights kept around 0. */
+typedef struct gdn_qk_norm {
+    const gdn_bf16 *q_weight, *k_weight;
+    float eps, add;
+} gdn_qk_norm;
+
+/*
+ * gdn_rope_freqs -- the rotary frequencies on the host: out[j] radians a
+ * position, j < rot/2, of f_j = base^(-2j/rot).
+ *   stretch 0  as they are
+ *   stretch 1  f_j / factor (positions interpolated)
+ *   stretch 2  base * factor^(rot / (rot - 2)) as the base (the longest
+ *              wavelength grows by factor, the shortest stays; rot > 2)
+ *   stretch 3  by wavelength (Peng et al., YaRN, 2023): with r = original *
+ *              f_j / 2 pi turns over the original context, keep f_j where r >=
+ *              high, f_j / factor where r <= low, and between them
+ *              g f_j + (1 - g) f_j / factor, g = (r - low) / (high - low)
+ * Host only.  GDN_ERR_NULL without out; GDN_ERR_SHAPE: rot negative or odd,
+ * base or factor not positive and finite, an unknown stretch, 2 with rot <= 2,
+ * 3 without original > 0 and high > low.
+ */
+gdn_status gdn_rope_freqs(int32_t rot, double base, int32_t stretch, double factor, double original, double low,
+                          double high, double *out);
+
+/*
+ * attn_prologue -- what comes between the projections and attention, in one
+ * launch (the packed attention prologue of the mstar pages: q/k norm, rotary
+ * positions, KV write): for every new token,
+ *   q_out = round(rotate(norm(q)));  k and v are stored into the token's cell,
+ *   k normed and rotated, v as it is; both divided by their scale, clamped to
+ *   +-448 and rounded to e4m3 in an 8-bit cache.
+ * Norm, rotation and scaling in fp32 with one rounding (to nearest even) at
+ * the end; the angle position * freq in fp64, so far positions keep their
+ * precision.
+ *
+ * q and q_out may both be NULL (only the cache is written) and so may k and v
+ * (only q turns; the page table is not read then).  q_out may be q itself;
+ * otherwise the two must not overlap.  positions [T] int32 or NULL: the angles'
+ * positions where they differ from the cache's.  norm and rope may be NULL.
+ * A token of a padding sequence (row 0) gets q_out +0.0 and writes nothing.
+ * A token whose row lies outside [0, R), whose position is negative or, where k
+ * and v are stored, past the table or on a page outside [1, N) gets NaN in
+ * q_out and writes nothing.  Tokens before cu_seqlens[0] or from
+ * cu_seqlens[B] on are left as they were.
+ * Preconditions, not checked: cu_seqlens is non-decreasing; no two tokens share
+ * a cell.  H_q, H_kv, d up to H_q + 2 H_kv <= 65535.
+ */
+gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
+                         const gdn_heads *q_out, const gdn_kv_cache *cache, const int32_t *row,
+                         const int32_t *cu_seqlens, const int32_t *positions, const gdn_rope *rope,
+                         const gdn_qk_norm *norm, hipStream_t stream);
+
+/*
+ * attn_paged -- attention of every new token over its row's cached tokens
+ * (the mixed step of mstar PR #965: prompt rows beside decode rows; the
+ * single-token form is n_b = 1).  The token at position p, query head h:
+ *   o = sum_j softmax_j(scale * q . k_j) v_j   over the positions
+ *   max(0, p - window + 1) <= j <= p           (0 <= j <= p without a window)
+ *   lse = log sum_j exp(scale * q . k_j)       (natural; lse may be NULL)
+ * q and k enter as they are, scores and the softmax's maximum and sum are fp32,
+ * weights are rounded to bf16 for the product with v (fp32 sums), o is rounded
+ * once.  A token that sees no position (kv_len < n_b, or a padding sequence on
+ * row 0) gets o = +0.0 and lse = -inf.  What lies in cells past kv_len, in
+ * later tokens' or in other rows' cells never shows, NaN and infinities
+ * included.  A sequence with a row outside [0, R), kv_len outside
+ * [0, table_width * page_size] or more than max_new tokens, and a token that
+ * needs a page outside [1, N), gets NaN in o and lse.  A sequence whose token
+ * range is not inside [0, T] is left as it was, and so are tokens outside
+ * [cu_seqlens[0], cu_seqlens[B]).
+ *
+ * q [T][H_q][d] and out by their strides; they must not overlap.  lse
+ * [T][H_q] fp32.  workspace: attn_paged_workspace_bytes(dims) bytes of device
+ * memory, 256-byte aligned, contents of no matter before and after; calls that
+ * share one must be stream-ordered.  The same call gives the same bits again.
+ * GDN_ERR_NULL, GDN_ERR_SHAPE (sizes, a workspace too small, scale not finite),
+ * GDN_ERR_UNSUPPORTED (d, page_size, cache_type, alignment).
+ */
+gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
+                      const int32_t *cu_seqlens, const gdn_heads *out, float *lse, float scale, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* The workspace attn_paged needs for dims (B, T, max_new, H_q, H_kv, d); 0 when
+ * dims is NULL or its sizes are unusable. */
+size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
+
+/*
+ * The cache's pages: which are free, who shares them, and moving them.  refs
+ * [N] int32 counts the table entries that name a page (0: free; refs[0] of the
+ * null page is ignored).  Bookkeeping runs on the device in stream order like
+ * slot_commit, so it can be captured with the step it belongs to.  A new page is
+ * always the free one with the lowest number, in the order of the list: the
+ * same calls give the same tables.  result [2] int32: how many listed rows
+ * were not served, and the first of them or -1; such a row and its pages are
+ * left as they were.
+ *
+ * gdn_pages: R, table_width, N, page_size as in gdn_attn_dims, page_table [R]
+ * [table_width], kv_len [R], refs [N].  For the calls that move pages: k and v of
+ * `layers` layers, page p of layer l at k + l*layer_stride + p*page_bytes
+ * (bytes; page_bytes a multiple of 16, v likewise, both 16-byte aligned).
+ * Preconditions, not checked: tables, lengths and refs agree.  Entries outside
+ * [1, N) are skipped.
+ */
+typedef struct gdn_pages {
+    int32_t R, table_width, N, page_size;
+    int32_t *page_table, *kv_len, *refs;
+    void *k, *v;
+    int32_t layers, reserved;
+    int64_t layer_stride, page_bytes;
+} gdn_pages;
+
+/* Device scratch of the calls below that take one: lists of up to n rows over
+ * R rows and N pages; 256-byte aligned, contents of no matter; calls that share
+ * it must be stream-ordered.  0 when a size is negative. */
+size_t kv_page_workspace_bytes(int32_t n, int32_t R, int32_t N);
+
+/*
+ * kv_page_reserve -- grow rows by their next tokens: kv_len[rows[i]] += add[i],
+ * with new pages behind the old ones where the last page does not hold them.
+ * Not served, in the order of the list: a row outside [1, R), one listed before,
+ * add[i] < 0, a length past the table, and, from the first one that the free
+ * pages do not suffice for, every row that needs a new page.  0 <= n <= 65535.
+ */
+gdn_status kv_page_reserve(const gdn_pages *pages, const int32_t *rows, const int32_t *add, int32_t n,
+                           int32_t *result, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kv_page_fork -- rows dst[i] become copies of rows src[i]: whole pages are
+ * shared (refs + 1), a last page that is partly filled is copied into a new
+ * one (every layer, k and v), so both rows can grow.  Not served: a row outside
+ * [1, R), src == dst, a dst that is not empty (kv_len 0; free it first) or is
+ * listed before, an unusable length, and, from the first one that the free pages do not
+ * suffice for, every fork that needs a new page.  A row may be the source of many.
+ */
+gdn_status kv_page_fork(const gdn_pages *pages, const int32_t *src, const int32_t *dst, int32_t n, int32_t *result,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kv_page_free -- the rows end: refs of their pages - 1, entries 0, kv_len 0.
+ * Row 0, rows outside [1, R) and a row listed twice are harmless.  Page
+ * contents stay as they are.
+ */
+gdn_status kv_page_free(const gdn_pages *pages, const int32_t *rows, int32_t n, hipStream_t stream);
+
+/*
+ * kv_page_copy -- page src[i] to page dst[i], bit for bit, in every layer, k
+ * and v (a prefix snapshot, as gdn_slot_copy for states).  Pairs with dst
+ * outside [1, N) or src outside [0, N) are skipped.  Preconditions: the
+ * destinations are distinct and none is a source.  page_table, kv_len and refs
+ * are not used.
+ */
+gdn_status kv_page_copy(const gdn_pages *pages, const int32_t *src, const int32_t *dst, int32_t n, hipStream_t stream);
+
+/*
+ * kv_page_compact -- the M pages with refs > 0 move into pages 1..M: each that
+ * lies above M, in ascending order, into the lowest hole; tables and refs
+ * follow.  remap [N] int32: a page's new number, 0 for a free one.  result [2]:
+ * M and how many pages moved.  The contents of left pages stay.
+ */
+gdn_status kv_page_compact(const gdn_pages *pages, int32_t *remap, int32_t *result, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
 /* Static text for a status code (host only). */
 const char *gdn_status_string(gdn_status status);
 

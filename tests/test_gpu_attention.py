@@ -1,0 +1,276 @@
+"""GPU: paged attention (attn_paged, through the binding) against 64-bit
+references: lengths around every block and page border, head groups, masks,
+strides, padding, unusable inputs, streams and captured graphs."""
+import math
+
+import pytest
+import torch
+
+from tests import attn_helpers as A
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import gated_deltanet_recurrent_decode_amd as m
+    m.lib()
+    return m
+
+
+def run(gdn, c, *, window=0, scale=None, max_new=None, q=None, out=None, lse=True, stream=None, ws=None, **over):
+    max_new = max([n for n, _ in c.lens] + [1]) if max_new is None else max_new
+    q = c.q.cuda() if q is None else q
+    out = torch.full((c.T, c.H_q, c.d), 7.0, dtype=A.BF, device="cuda") if out is None else out
+    L = torch.full((c.T, c.H_q), 7.0, device="cuda") if lse else None
+    if ws is None:
+        ws = torch.full((gdn.attn_paged_workspace_bytes(c.B, c.T, max_new, c.H_q, c.H_kv, c.d),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+    a = c.cuda(**over)
+    gdn.attn_paged(q, a["k_pages"], a["v_pages"], a["page_table"], a["kv_len"], a["row"], a["cu_seqlens"], out, ws,
+                   max_new=max_new, scale=scale, window=window, lse=L, k_scale=a["k_scale"], v_scale=a["v_scale"],
+                   stream=stream)
+    torch.cuda.synchronize()
+    return out, L
+
+
+def both(gdn, c, window=0, **kw):
+    out, lse = run(gdn, c, window=window, **kw)
+    o, l, tol, tol_l = A.attention(c, c.d ** -0.5, window)
+    A.check(out, o, tol, "out")
+    A.check(lse, l, tol_l, "lse")
+    return out, lse
+
+
+BORDERS = [(1, p) for p in (0, 1, 14, 15, 16, 30, 31, 32, 63, 64, 126, 127, 128, 255, 300)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_single_tokens_at_every_border(gdn, d, kind, page):
+    both(gdn, A.Cache(BORDERS, H_q=4, H_kv=2, d=d, page=page, kind=kind, seed=d + page))
+
+
+@pytest.mark.parametrize("G", [1, 3, 5, 8, 16, 20])
+def test_head_groups(gdn, G):
+    both(gdn, A.Cache([(1, 70), (2, 40), (5, 0)], H_q=2 * G, H_kv=2, d=128, page=32, seed=G))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 1, 17, 100])
+def test_ragged_chunks(gdn, d, kind, window):
+    c = A.Cache([(70, 0), (1, 300), (0, 5), (33, 64), (4, 130), (129, 77), (16, 16)], H_q=6, H_kv=2, d=d, page=32,
+                kind=kind, seed=window)
+    both(gdn, c, window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_long_context_is_cut_and_joined(gdn, d, kind):
+    # one sequence over every workgroup, and a short one beside it
+    both(gdn, A.Cache([(1, 20011), (1, 9)], H_q=4, H_kv=1, d=d, page=64, kind=kind, seed=5))
+
+
+def test_chunk_behind_a_long_context(gdn):
+    both(gdn, A.Cache([(257, 3000)], H_q=4, H_kv=1, d=128, page=64, seed=6))
+
+
+def test_many_sequences(gdn):
+    # more than one round of the scan over sequences, some empty
+    lens = [((i * 7) % 3, (i * 37) % 150) for i in range(601)]
+    both(gdn, A.Cache(lens, H_q=2, H_kv=1, d=64, page=16, seed=8))
+
+
+def test_large_scores_and_a_dominant_key(gdn):
+    c = A.Cache([(3, 200)], H_q=4, H_kv=2, d=128, page=16, seed=9, q_scale=30.0)
+    both(gdn, c)
+
+
+def test_strided_queries_and_outputs(gdn):
+    c = A.Cache([(3, 50), (1, 20)], H_q=6, H_kv=2, d=64, page=16, seed=10)
+    wide = torch.full((c.T, 6, 3 * 64), 5.0, dtype=A.BF, device="cuda")
+    wide[:, :, 64:128] = c.q.cuda()
+    target = torch.full((c.T, 8, 2 * 64), 7.0, dtype=A.BF, device="cuda")
+    before = target.clone()
+    out, _ = run(gdn, c, q=wide[:, :, 64:128], out=target[:, 1:7, 64:])
+    o, _, tol, _ = A.attention(c, 64 ** -0.5)
+    A.check(target[:, 1:7, 64:], o, tol, "out")
+    target[:, 1:7, 64:] = 7.0
+    assert torch.equal(target, before), "written outside the output's heads"
+    run(gdn, c, lse=False)
+
+
+def test_rows_that_see_nothing(gdn):
+    # fewer cached tokens than new ones: the first tokens see no position
+    c = A.Cache([(6, 0), (2, 4)], H_q=4, H_kv=2, d=64, page=16, seed=11)
+    c.kv_len[int(c.row[0])] = 4
+    out, lse = both(gdn, c)
+    assert (out[:2] == 0).all() and (lse[:2] == -math.inf).all()
+    c.kv_len[int(c.row[0])] = 0
+    both(gdn, c)
+
+
+def test_padding_and_unusable_sequences(gdn):
+    lens = [(1, 40), (2, 30), (1, 20), (3, 10), (1, 50), (2, 60)]
+    c = A.Cache(lens, H_q=4, H_kv=2, d=64, page=16, seed=12)
+    want, want_lse, tol, tol_l = A.attention(c, 64 ** -0.5)
+    row, table, kv_len = c.row.clone(), c.table.clone(), c.kv_len.clone()
+    row[0] = 0                                     # padding
+    row[1] = c.R                                   # outside the table
+    kv_len[int(row[2])] = c.width * c.page + 1     # longer than the table
+    table[int(row[4]), 1] = c.N                    # a page outside the pool
+    table[int(row[5]), 0] = 0                      # no page, seen by both tokens
+    out, lse = run(gdn, c, row=row, page_table=table, kv_len=kv_len, max_new=2)  # sequence 3 has more tokens
+    assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
+    for t in (1, 2, 3, 4, 5, 6, 7, 8, 9):
+        assert out[t].isnan().all() and lse[t].isnan().all(), t
+    # the same without what is unusable
+    out, lse = run(gdn, c)
+    A.check(out, want, tol, "out")
+
+
+def test_a_bad_page_behind_the_window_or_later_does_not_show(gdn):
+    c = A.Cache([(20, 60)], H_q=2, H_kv=1, d=64, page=16, seed=13)
+    table = c.table.clone()
+    table[int(c.row[0]), 0] = -5     # positions 0..15
+    table[int(c.row[0]), 4] = c.N    # positions 64..79
+    out, lse = run(gdn, c, window=20, page_table=table)
+    want, _, tol, _ = A.attention(c, 64 ** -0.5, 20)
+    # token i stands at 60 + i and sees 41 + i .. 60 + i: the first four miss position 64
+    A.check(out[:4], want[:4], tol[:4], "out")
+    assert out[4:].isnan().all()
+
+
+def test_rows_outside_the_sequences_stay(gdn):
+    c = A.Cache([(2, 40), (3, 30)], H_q=4, H_kv=2, d=64, page=16, seed=14)
+    cu = c.cu + 4
+    q = torch.zeros(c.T + 9, 4, 64, dtype=A.BF, device="cuda")
+    q[4:4 + c.T] = c.q.cuda()
+    out = torch.full_like(q, 7.0)
+    big = A.Cache([(2, 40), (3, 30)], H_q=4, H_kv=2, d=64, page=16, seed=14)
+    big.T = c.T + 9
+    got, lse = run(gdn, big, q=q, out=out, cu_seqlens=cu)
+    want, _, tol, _ = A.attention(c, 64 ** -0.5)
+    A.check(got[4:4 + c.T], want, tol, "out")
+    assert (got[:4] == 7).all() and (got[4 + c.T:] == 7).all()
+    assert (lse[:4] == 7).all() and (lse[4 + c.T:] == 7).all()
+    # a sequence whose range leaves the packed tokens
+    cu2 = cu.clone()
+    cu2[2] = big.T + 1
+    got, _ = run(gdn, big, q=q, cu_seqlens=cu2)
+    A.check(got[4:6], want[:2], tol[:2], "out")
+    assert (got[6:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("n", [6, 150])
+def test_a_later_tokens_nan_stays_its_own(gdn, kind, bad, n):
+    if kind == "e4m3" and math.isinf(bad):
+        pytest.skip("e4m3 has no infinity")
+    c = A.Cache([(n, 40)], H_q=4, H_kv=2, d=128, page=16, kind=kind, seed=15)
+    r = int(c.row[0])
+    for pos, col in ((42, 3), (40 + n - 1, 77)):
+        c.v[int(c.table[r, pos // 16]), :, pos % 16, col] = bad
+    c.k[int(c.table[r, (40 + n - 2) // 16]), 1, (40 + n - 2) % 16] = math.nan
+    for window in (0, 16):
+        out, lse = run(gdn, c, window=window)
+        want, want_lse, tol, tol_l = A.attention(c, 128 ** -0.5, window)
+        # a NaN among the keys makes every output of the tokens that see it NaN
+        A.check(out[:, :2], want[:, :2], tol[:, :2], "out")
+        A.check(out[:n - 2, 2:], want[:n - 2, 2:], tol[:n - 2, 2:], "out")
+        assert out[n - 2:, 2:].isnan().all() and lse[n - 2:, 2:].isnan().all()
+
+
+def test_the_same_bits_again_in_any_workspace_and_stream(gdn):
+    c = A.Cache([(1, 5000), (40, 700), (1, 3)], H_q=8, H_kv=2, d=128, page=32, seed=16)
+    first, lse = run(gdn, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again, lse2 = run(gdn, c, stream=side)
+    assert torch.equal(first.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+    # a larger call between them leaves its parts in the workspace
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(1, 1, 64, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    run(gdn, A.Cache([(1, 30000)], H_q=8, H_kv=2, d=128, page=32, seed=17), ws=ws, max_new=64)
+    again, _ = run(gdn, c, ws=ws, max_new=64)
+    assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+def test_the_order_of_the_sequences_does_not_matter(gdn):
+    c = A.Cache([(1, 500), (4, 700), (1, 3), (9, 90)], H_q=8, H_kv=2, d=64, page=32, seed=18)
+    both(gdn, c)
+    order = [2, 0, 3, 1]
+    e = A.Cache([c.lens[i] for i in order], H_q=8, H_kv=2, d=64, page=32, seed=18)
+    e.k, e.v, e.table, e.kv_len, e.N, e.R, e.width = c.k, c.v, c.table, c.kv_len, c.N, c.R, c.width
+    e.row = c.row[order]
+    e.q = torch.cat([c.q[int(c.cu[i]):int(c.cu[i + 1])] for i in order])
+    both(gdn, e)
+
+
+def test_a_captured_step_follows_its_lengths(gdn):
+    """One graph, replayed while the rows grow, a row turns to padding and pages move."""
+    lens = [(1, 30), (1, 140), (1, 900), (1, 0)]
+    c = A.Cache(lens, H_q=8, H_kv=2, d=128, page=16, seed=19, width=70)
+    a = c.cuda()
+    q, out = c.q.cuda(), torch.empty(c.T, 8, 128, dtype=A.BF, device="cuda")
+    lse = torch.empty(c.T, 8, device="cuda")
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(c.B, c.T, 1, 8, 2, 128), dtype=torch.uint8, device="cuda")
+
+    def call():
+        gdn.attn_paged(q, a["k_pages"], a["v_pages"], a["page_table"], a["kv_len"], a["row"], a["cu_seqlens"], out,
+                       ws, max_new=1, lse=lse)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in range(4):
+        m = A.Cache([(1, p + 37 * step) for _, p in lens], H_q=8, H_kv=2, d=128, page=16, seed=20 + step, spare=3,
+                    width=70)
+        pool = min(m.N, c.N) if m.N > c.N else m.N
+        if m.N > c.N:  # the captured pool is as large as the first one: keep to its pages
+            m = A.Cache([(1, max(0, p - 16 * step)) for _, p in lens], H_q=8, H_kv=2, d=128, page=16,
+                        seed=20 + step, spare=3, width=70)
+            pool = m.N
+        for name, x in (("k_pages", m.k), ("v_pages", m.v)):
+            a[name][:pool].copy_(x)
+        a["page_table"].copy_(m.table)
+        a["kv_len"].copy_(m.kv_len)
+        a["row"].copy_(m.row)
+        q.copy_(m.q)
+        if step == 2:
+            a["row"][1] = 0
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_lse, tol, tol_l = A.attention(m, 128 ** -0.5)
+        if step == 2:
+            want[1], want_lse[1] = 0, -math.inf
+        A.check(out, want, tol, f"replay {step}")
+        A.check(lse, want_lse, tol_l, f"replay {step}")
+        call()
+        eager = out.clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager.view(torch.int16), out.view(torch.int16))
+
+
+def test_pages_past_four_gigabytes(gdn):
+    """Cells whose byte offsets pass 32 bits: a 5 GiB pool with the sequence at its top."""
+    d, H_kv, page = 256, 2, 256
+    N = (5 << 30) // (H_kv * page * d * 2)
+    c = A.Cache([(3, 700)], H_q=8, H_kv=H_kv, d=d, page=page, seed=21)
+    k = torch.zeros(N, H_kv, page, d, dtype=A.BF, device="cuda")
+    v = torch.zeros(N, H_kv, page, d, dtype=A.BF, device="cuda")
+    up = N - c.N
+    k[up:], v[up:] = c.k.cuda(), c.v.cuda()
+    table = torch.where(c.table > 0, c.table + up, 0).to(torch.int32).cuda()
+    q, out = c.q.cuda(), torch.empty(c.T, 8, d, dtype=A.BF, device="cuda")
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(1, c.T, 3, 8, H_kv, d), dtype=torch.uint8, device="cuda")
+    gdn.attn_paged(q, k, v, table, c.kv_len.cuda(), c.row.cuda(), c.cu.cuda(), out, ws, max_new=3)
+    want, _, tol, _ = A.attention(c, d ** -0.5)
+    A.check(out, want, tol, "out")
