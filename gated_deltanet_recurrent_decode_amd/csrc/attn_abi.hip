@@ -164,7 +164,7 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims)
     if (d.B < 0 || d.T < 0 || d.max_new < 0 || d.H_q < 1 || d.H_kv < 1 || d.H_q % d.H_kv != 0 ||
         (d.d != 64 && d.d != 128 && d.d != 256))
         return 0;
-    return gdn::attn_paged_layout(d.max_new, d.H_q / d.H_kv, d.d, nullptr, nullptr);
+    return gdn::attn_paged_layout(d.B, d.T, d.max_new, d.H_kv, d.H_q / d.H_kv, d.d, nullptr, nullptr);
 }
 
 gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
@@ -190,7 +190,7 @@ gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_k
     if (!isfinite(scale))
         return GDN_ERR_SHAPE;
     gdn::AttnParams p{};
-    if (workspace_bytes < gdn::attn_paged_layout(d.max_new, d.H_q / d.H_kv, d.d, workspace, &p))
+    if (workspace_bytes < gdn::attn_paged_layout(d.B, d.T, d.max_new, d.H_kv, d.H_q / d.H_kv, d.d, workspace, &p))
         return GDN_ERR_SHAPE;
     p.q = heads_of(*q);
     p.out = heads_of(*out);

@@ -32,6 +32,58 @@ __device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t v)
 
 __device__ __forceinline__ float min_finite(float x, float top) { return x > top ? top : (x < -top ? -top : x); }
 
+// Ends a chain of matrix products: the result is in vector registers, read behind the waits
+// that the matrix cores need, before any branch.  Without it the compiler has put the reads
+// behind a branch with too few waits on its taken side (wrong scores, every time).
+template <class T>
+__device__ __forceinline__ void settle(T &x)
+{
+    asm volatile("" : "+v"(x));
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+enum { kSkip = -1, kNormal = 0, kZero = 1, kNan = 2 };
+
+// A sequence of the call as the arrays on the device give it.
+struct Seq {
+    int kind, first, n, L, lo; // first token, tokens, keys, first key in reach of the window
+    int r;                     // row of the table
+};
+
+__device__ __forceinline__ Seq read_seq(const AttnParams &p, int b)
+{
+    Seq s;
+    s.first = p.cu[b];
+    const int e = p.cu[b + 1];
+    s.n = e - s.first;
+    s.kind = kNormal;
+    s.r = p.row[b];
+    s.L = s.lo = 0;
+    if (s.first < 0 || e > p.T || e <= s.first) {
+        s.kind = kSkip;
+        return s;
+    }
+    if (s.r == 0) {
+        s.kind = kZero;
+    } else if (s.r < 0 || s.r >= p.R || s.n > p.max_new) {
+        s.kind = kNan;
+    } else {
+        s.L = p.kv_len[s.r];
+        if (s.L < 0 || s.L > (p.width << p.page_shift)) {
+            s.kind = kNan;
+            s.L = 0;
+        } else if (p.window > 0 && s.L - s.n - p.window + 1 > 0) {
+            s.lo = (s.L - s.n - p.window + 1) & ~31;
+        }
+    }
+    return s;
+}
+
+// log2 of a sum relative to a maximum, as a natural logarithm
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994530942f;
+}
 
 } // namespace gdn

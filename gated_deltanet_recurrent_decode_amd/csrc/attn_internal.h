@@ -34,6 +34,10 @@ struct AttnParams {
     float scale;                // in the exponent of 2
     int B, T, R, H_q, H_kv, G, N, page_shift, width, max_new, window;
     int workgroups;
+    long long *before;          // tiles: units of the call before each entry, and the sum of all
+    int32_t *entry;             // tiles: [entries][3] sequence, kv head, tile
+    int32_t *count;             // tiles: entries
+    int block;                  // tiles: keys of a block
 };
 
 struct PageParams {
@@ -51,7 +55,12 @@ struct PageParams {
 
 hipError_t launch_attn_prologue(const AttnPrologueParams &p, int d, bool e4m3, hipStream_t stream);
 // device scratch in bytes; fills the parameter block's pointers when it is given
-size_t attn_paged_layout(int max_new, int G, int d, void *base, AttnParams *p);
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p);
+size_t attn_rows_layout(int d, void *base, AttnParams *p);
+size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnParams *p);
+hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
+hipError_t launch_attn_tiles(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
 hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
 hipError_t launch_kv_reserve(const PageParams &p, hipStream_t stream);
 hipError_t launch_kv_fork(const PageParams &p, hipStream_t stream);

@@ -33,48 +33,22 @@ constexpr int TM = 16;    // rows of a tile
 constexpr int UNIT = 128; // keys of a unit: a block of 32 a wave
 constexpr int NT = 256;
 
-enum { kSkip = -1, kNormal = 0, kZero = 1, kNan = 2 };
-
-struct Seq {
-    int kind, first, n, L, lo; // first token, tokens, keys, first key in reach of the window
-    int r;                     // row of the table
-    int tiles, units;          // tiles of rows, units of a tile
+// A sequence's tiles of rows, and the units of each of them.
+struct RowSeq : Seq {
+    int tiles, units;
 };
 
-__device__ __forceinline__ Seq read_seq(const AttnParams &p, int b)
+__device__ __forceinline__ RowSeq read_row_seq(const AttnParams &p, int b)
 {
-    Seq s;
-    s.first = p.cu[b];
-    const int e = p.cu[b + 1];
-    s.n = e - s.first;
-    s.kind = kNormal;
-    s.r = p.row[b];
-    s.L = s.lo = 0;
-    s.tiles = s.units = 0;
-    if (s.first < 0 || e > p.T || e <= s.first) {
-        s.kind = kSkip;
-        return s;
-    }
-    if (s.r == 0) {
-        s.kind = kZero;
-    } else if (s.r < 0 || s.r >= p.R || s.n > p.max_new) {
-        s.kind = kNan;
-    } else {
-        s.L = p.kv_len[s.r];
-        if (s.L < 0 || s.L > (p.width << p.page_shift)) {
-            s.kind = kNan;
-            s.L = 0;
-        } else if (p.window > 0 && s.L - s.n - p.window + 1 > 0) {
-            s.lo = (s.L - s.n - p.window + 1) & ~31;
-        }
-    }
-    s.tiles = (int)(((int64_t)s.n * p.G + TM - 1) / TM);
+    RowSeq s;
+    static_cast<Seq &>(s) = read_seq(p, b);
     const int span = s.L - s.lo;
+    s.tiles = s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TM - 1) / TM);
     s.units = span > UNIT ? (span + UNIT - 1) / UNIT : 1;
     return s;
 }
 
-__device__ __forceinline__ long long seq_units(const AttnParams &p, const Seq &s)
+__device__ __forceinline__ long long seq_units(const AttnParams &p, const RowSeq &s)
 {
     return (long long)p.H_kv * s.tiles * s.units;
 }
@@ -101,10 +75,10 @@ __device__ Place locate(const AttnParams &p, Hit hit)
         long long run = 0;
         for (int b0 = 0; b0 < p.B; b0 += NT) {
             const int b = b0 + tid;
-            Seq s;
+            RowSeq s;
             long long u = 0;
             if (b < p.B) {
-                s = read_seq(p, b);
+                s = read_row_seq(p, b);
                 u = seq_units(p, s);
             }
             long long inc = u;
@@ -158,12 +132,6 @@ __device__ __forceinline__ int owner_of(long long total, long long u, int pieces
     return (int)(((u + 1) * pieces - 1) / total);
 }
 
-// log2 of a sum relative to a maximum, as a natural logarithm
-__device__ __forceinline__ float lse_of(float m, float l)
-{
-    return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994530942f;
-}
-
 } // namespace
 
 // D = 64, 128 or 256.  A lane owns EV consecutive columns of v in each of NH
@@ -180,7 +148,7 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
     const int n_ = lane & 15, g = lane >> 4;
     const int w = blockIdx.x;
 
-    const Place at = locate(p, [&](const Seq &, long long before, long long units, long long total) {
+    const Place at = locate(p, [&](const RowSeq &, long long before, long long units, long long total) {
         const int pieces = pieces_of(p, total);
         const long long u0 = piece(total, w, pieces);
         return w < pieces && before <= u0 && u0 < before + units;
@@ -195,7 +163,7 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
     long long before = at.before;
 
     while (u < u_end) {
-        const Seq s = read_seq(p, b);
+        const RowSeq s = read_row_seq(p, b);
         const long long units = seq_units(p, s);
         if (u >= before + units) {
             before += units;
@@ -317,6 +285,9 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
                             vr[a][j][c] = reinterpret_cast<const uint32_t *>(vp)[c];
                     }
                 }
+
+            settle(sc[0]);
+            settle(sc[1]);
 
             // masks, where some row of the tile does not see every key of the block
             const bool mixed = key0 + 31 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
@@ -499,12 +470,12 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams p)
     constexpr int E = D / 64;
     const int t = blockIdx.x, h = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Place at = locate(p, [&](const Seq &s, long long, long long, long long) {
+    const Place at = locate(p, [&](const RowSeq &s, long long, long long, long long) {
         return t >= s.first && t < s.first + s.n;
     });
     if (at.b < 0)
         return;
-    const Seq s = read_seq(p, at.b);
+    const RowSeq s = read_row_seq(p, at.b);
     const int pieces = pieces_of(p, at.total);
     for (int q = wave; q < p.G; q += 4) {
         const int row = (t - s.first) * p.G + q;
@@ -546,12 +517,8 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams p)
     }
 }
 
-static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
-size_t attn_paged_layout(int max_new, int G, int d, void *base, AttnParams *p)
+size_t attn_rows_layout(int d, void *base, AttnParams *p)
 {
-    (void)max_new;
-    (void)G;
     const int workgroups = 2 * device_cus();
     const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4);
     if (p) {
@@ -575,13 +542,30 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     return e;
 }
 
-hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
+hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
     if (d == 64)
         return e4m3 ? launch_de<64, true>(p, stream) : launch_de<64, false>(p, stream);
     if (d == 128)
         return e4m3 ? launch_de<128, true>(p, stream) : launch_de<128, false>(p, stream);
     return e4m3 ? launch_de<256, true>(p, stream) : launch_de<256, false>(p, stream);
+}
+
+// Up to this many rows a sequence the kernel of 16-row tiles is used: it reads a
+// sequence's keys once per tile, the other once for 256 rows but through LDS.
+constexpr int kFewRows = 64;
+
+size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)
+{
+    if ((int64_t)max_new * G <= kFewRows)
+        return attn_rows_layout(d, base, p);
+    return attn_tiles_layout(B, T, H_kv, G, d, base, p);
+}
+
+hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
+{
+    return (int64_t)p.max_new * p.G <= kFewRows ? launch_attn_rows(p, d, e4m3, stream)
+                                                : launch_attn_tiles(p, d, e4m3, stream);
 }
 
 } // namespace gdn
