@@ -11,8 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
-from . import GdnError, _check, _contig, _dev, _device, _on, _ptr, _stream, _torch, lib
+from . import GdnError, _check, lib
 
 EXPORTS = ("gdn_rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "kv_page_workspace_bytes",
            "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact")
@@ -48,89 +49,165 @@ class Pages(ctypes.Structure):
                 [("layers", _i32), ("reserved", _i32), ("layer_stride", _i64), ("page_bytes", _i64)])
 
 
+# The same structures as packed bytes: filling a ctypes structure field by field takes longer than the
+# smallest of these calls takes on the GPU.
+_DIMS, _HEADS, _CACHE = struct.Struct("12i"), struct.Struct("Pqq"), struct.Struct("6P")
+_ROPE, _NORM, _PAGES = struct.Struct("Piif4x"), struct.Struct("PPff"), struct.Struct("4i5P2i2q")
+for _packed, _struct in ((_DIMS, AttnDims), (_HEADS, Heads), (_CACHE, KvCache), (_ROPE, Rope), (_NORM, QkNorm),
+                         (_PAGES, Pages)):
+    assert _packed.size == ctypes.sizeof(_struct), _struct
+
+
 def declare(L) -> None:
-    """Argument types of this module's entry points."""
-    D, H, C, G = (ctypes.POINTER(t) for t in (AttnDims, Heads, KvCache, Pages))
+    """Argument types of this module's entry points (structures go as pointers or as packed bytes)."""
     size = ctypes.c_size_t
     for name, args, res in (
             ("gdn_rope_freqs", [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _P], _i32),
-            ("attn_prologue", [D, H, H, H, H, C, _P, _P, _P, ctypes.POINTER(Rope), ctypes.POINTER(QkNorm), _P], _i32),
-            ("attn_paged", [D, H, C, _P, _P, H, _P, _f32, _P, size, _P], _i32),
-            ("attn_paged_workspace_bytes", [D], size),
+            ("attn_prologue", [_P] * 12, _i32),
+            ("attn_paged", [_P, _P, _P, _P, _P, _P, _P, _f32, _P, size, _P], _i32),
+            ("attn_paged_workspace_bytes", [_P], size),
             ("kv_page_workspace_bytes", [_i32, _i32, _i32], size),
-            ("kv_page_reserve", [G, _P, _P, _i32, _P, _P, size, _P], _i32),
-            ("kv_page_fork", [G, _P, _P, _i32, _P, _P, size, _P], _i32),
-            ("kv_page_free", [G, _P, _i32, _P], _i32),
-            ("kv_page_copy", [G, _P, _P, _i32, _P], _i32),
-            ("kv_page_compact", [G, _P, _P, _P, size, _P], _i32)):
+            ("kv_page_reserve", [_P, _P, _P, _i32, _P, _P, size, _P], _i32),
+            ("kv_page_fork", [_P, _P, _P, _i32, _P, _P, size, _P], _i32),
+            ("kv_page_free", [_P, _P, _i32, _P], _i32),
+            ("kv_page_copy", [_P, _P, _P, _i32, _P], _i32),
+            ("kv_page_compact", [_P, _P, _P, _P, size, _P], _i32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
 
-# ------------------------------------------------------------------ checks
+# ------------------------------------------------------------------ tensors as pointers
 
-def _cache_type(k_pages, v_pages):
+_module = None
+
+
+def _torch():
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
+
+
+def _refuse(t, name, dtype, device):
+    """Why `t` cannot be used (the checks of the fast paths below, with their messages)."""
     torch = _torch()
-    if k_pages.dtype != v_pages.dtype or k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError(f"k_pages and v_pages must both be bfloat16 or float8_e4m3fn, got {k_pages.dtype}, "
-                         f"{v_pages.dtype}")
-    return int(k_pages.dtype == torch.float8_e4m3fn)
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a GPU tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"all tensors must be on one GPU, got {name} on {t.device} and others on cuda:{device}")
+    raise ValueError(f"{name}: must be contiguous")
 
+
+def _gpu(t, name, dtype):
+    """The index of the GPU that `t` is on."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+        _refuse(t, name, dtype, -1)
+    return t.get_device()
+
+
+def _at(t, name, dtype, device):
+    """A contiguous tensor's address."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, device)
+
+
+def _at_or_none(t, name, dtype, device):
+    return 0 if t is None else _at(t, name, dtype, device)
+
+
+def _strided(t, name, dtype, device):
+    """Packed heads as the C structure: address, row and head strides."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, dtype, device)
+    s = t.stride()
+    return _HEADS.pack(t.data_ptr(), s[0], s[1])
+
+
+def _launch(name, call, device, stream, *args):
+    """Call with the stream to launch on, with the tensors' GPU as the current HIP device."""
+    torch = _torch()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
+        raw = stream.cuda_stream
+    now = torch._C._cuda_getDevice()
+    if now == device:
+        status = call(*args, raw)
+    else:
+        torch.cuda.set_device(device)
+        try:
+            status = call(*args, raw)
+        finally:
+            torch.cuda.set_device(now)
+    if status:
+        _check(name, status)
+
+
+# ------------------------------------------------------------------ checks
 
 def _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale):
     """Shape checks of a layer's cache (any device); returns N, H_kv, page_size, d, R, width, cache_type."""
-    kind = _cache_type(k_pages, v_pages)
-    shape = k_pages.shape
+    torch = _torch()
+    dtype, shape = k_pages.dtype, k_pages.shape
+    if v_pages.dtype is not dtype or dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"k_pages and v_pages must both be bfloat16 or float8_e4m3fn, got {dtype}, {v_pages.dtype}")
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must both be [N][H_kv][page_size][d]")
     N, H_kv, page, d = shape
-    R = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    rows = kv_len.shape
+    if len(rows) != 1:
+        raise ValueError("kv_len must be [R]")
     width = 1
     if page_table is not None:
-        if page_table.dim() != 2 or page_table.shape[0] != R:
+        table = page_table.shape
+        if len(table) != 2 or table[0] != rows[0]:
             raise ValueError("page_table must be [R][width] and kv_len [R]")
-        width = page_table.shape[1]
-    elif R < 0:
-        raise ValueError("kv_len must be [R]")
-    if kind:
+        width = table[1]
+    kind = 0
+    if dtype is torch.float8_e4m3fn:
+        kind = 1
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None or tuple(t.shape) != (H_kv,):
+            if t is None or t.shape != (H_kv,):
                 raise ValueError(f"{n} [H_kv] is required for an e4m3 cache")
-    return N, H_kv, page, d, R, width, kind
+    return N, H_kv, page, d, rows[0], width, kind
+
+
+def _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev):
+    """A layer's cache as the C structure."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    return _CACHE.pack(_at(k_pages, "k_pages", k_pages.dtype, dev), _at(v_pages, "v_pages", v_pages.dtype, dev),
+                       _at_or_none(k_scale, "k_scale", f32, dev), _at_or_none(v_scale, "v_scale", f32, dev),
+                       _at_or_none(page_table, "page_table", i32, dev), _at(kv_len, "kv_len", i32, dev))
 
 
 def _packed_layout(row, cu_seqlens):
-    if row.dim() != 1 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != row.shape[0] + 1:
+    a, b = row.shape, cu_seqlens.shape
+    if len(a) != 1 or len(b) != 1 or b[0] != a[0] + 1:
         raise ValueError("row must be [B] and cu_seqlens [B+1]")
-    return row.shape[0]
+    return a[0]
 
 
 def _heads_layout(t, name, T, H, d):
     """[T][H][d] with contiguous d; returns H."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or (H is not None and t.shape[1] != H):
-        raise ValueError(f"{name} must be [{T}][{'H' if H is None else H}][{d}], got {list(t.shape)}")
-    if t.stride(2) != 1 and d > 1:
+    s = t.shape
+    if len(s) != 3 or s[0] != T or s[2] != d or (H is not None and s[1] != H):
+        raise ValueError(f"{name} must be [{T}][{'H' if H is None else H}][{d}], got {list(s)}")
+    if t.stride(2) != 1:
         raise ValueError(f"{name}: the head's values must be contiguous")
-    return t.shape[1]
-
-
-def _heads(t):
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _ints(t, name):
-    return _contig(_dev(t, name, _torch().int32), name)
-
-
-def _check_cache_tensors(k_pages, v_pages, page_table, kv_len, k_scale, v_scale):
-    torch = _torch()
-    _contig(_dev(k_pages, "k_pages", k_pages.dtype), "k_pages")
-    _contig(_dev(v_pages, "v_pages", v_pages.dtype), "v_pages")
-    if page_table is not None:
-        _ints(page_table, "page_table")
-    _ints(kv_len, "kv_len")
-    _contig(_dev(k_scale, "k_scale", torch.float32, allow_none=True), "k_scale")
-    _contig(_dev(v_scale, "v_scale", torch.float32, allow_none=True), "v_scale")
+    return s[1]
 
 
 # ------------------------------------------------------------------ entry points
@@ -157,55 +234,50 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
     like q (or q itself); freqs [rot/2] float64 or None; row [B], cu_seqlens [B+1] int32.  q and q_out may be
     None, and so may k and v (page_table may then be None too)."""
     torch = _torch()
-    bf = torch.bfloat16
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     if q is None and k is None:
         raise ValueError("nothing to do: q or k and v are required")
     if (q is None) != (q_out is None) or (k is None) != (v is None):
         raise ValueError("q and q_out go together, and so do k and v")
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
     B = _packed_layout(row, cu_seqlens)
-    T = (q if q is not None else k).shape[0]
+    dev = _gpu(row, "row", i32)
+    hq = ho = hk = hv = rope = norm = None
     H_q = H_kv
     if q is not None:
-        H_q = _heads_layout(_dev(q, "q", bf), "q", T, None, d)
-        _heads_layout(_dev(q_out, "q_out", bf), "q_out", T, H_q, d)
+        T = q.shape[0]
+        H_q = _heads_layout(q, "q", T, None, d)
+        _heads_layout(q_out, "q_out", T, H_q, d)
+        hq, ho = _strided(q, "q", bf, dev), _strided(q_out, "q_out", bf, dev)
     if k is not None:
+        T = k.shape[0] if q is None else T
         if page_table is None:
             raise ValueError("page_table is required to store k and v")
-        _heads_layout(_dev(k, "k", bf), "k", T, H_kv, d)
-        _heads_layout(_dev(v, "v", bf), "v", T, H_kv, d)
-    _check_cache_tensors(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
-    _ints(row, "row")
-    _ints(cu_seqlens, "cu_seqlens")
-    if positions is not None and tuple(_ints(positions, "positions").shape) != (T,):
-        raise ValueError("positions must be [T]")
-    rope = norm = None
+        _heads_layout(k, "k", T, H_kv, d)
+        _heads_layout(v, "v", T, H_kv, d)
+        hk, hv = _strided(k, "k", bf, dev), _strided(v, "v", bf, dev)
     if freqs is not None:
-        _contig(_dev(freqs, "freqs", torch.float64), "freqs")
         if freqs.dim() != 1 or 2 * freqs.shape[0] > d:
             raise ValueError("freqs must be [rot/2] with rot <= d")
-        rope = ctypes.byref(Rope(freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)), rope_scale))
-    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None and tuple(_contig(_dev(t, n, bf), n).shape) != (d,):
-            raise ValueError(f"{n} must be [d]")
+        rope = _ROPE.pack(_at(freqs, "freqs", torch.float64, dev), 2 * freqs.shape[0], int(bool(interleaved)),
+                          rope_scale)
     if q_norm is not None or k_norm is not None:
-        norm = ctypes.byref(QkNorm(q_norm.data_ptr() if q_norm is not None else None,
-                                   k_norm.data_ptr() if k_norm is not None else None, norm_eps, norm_add))
-    dev = _device(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, freqs, q_norm, k_norm,
-                  positions, k_scale, v_scale)
-    dims = AttnDims(B, T, R, H_q, H_kv, d, N, page, width, 0, 0, kind)
-    cache = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-                    kv_len.data_ptr())
-    hq, hk, hv, ho = (None if t is None else ctypes.byref(_heads(t)) for t in (q, k, v, q_out))
-    with _on(dev):
-        _check("attn_prologue", lib().attn_prologue(
-            ctypes.byref(dims), hq, hk, hv, ho, ctypes.byref(cache), row.data_ptr(), cu_seqlens.data_ptr(),
-            _ptr(positions), rope, norm, _stream(stream, dev)))
+        for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None and t.shape != (d,):
+                raise ValueError(f"{n} must be [d]")
+        norm = _NORM.pack(_at_or_none(q_norm, "q_norm", bf, dev), _at_or_none(k_norm, "k_norm", bf, dev), norm_eps,
+                          norm_add)
+    if positions is not None and positions.shape != (T,):
+        raise ValueError("positions must be [T]")
+    _launch("attn_prologue", lib().attn_prologue, dev, stream,
+            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, 0, 0, kind), hq, hk, hv, ho,
+            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev), _at(row, "row", i32, dev),
+            _at(cu_seqlens, "cu_seqlens", i32, dev), _at_or_none(positions, "positions", i32, dev), rope, norm)
 
 
 def attn_paged_workspace_bytes(B: int, T: int, max_new: int, H_q: int, H_kv: int, d: int) -> int:
     """The workspace attn_paged needs (see include/gdn.h), in bytes, on the current GPU."""
-    n = lib().attn_paged_workspace_bytes(ctypes.byref(AttnDims(B, T, 1, H_q, H_kv, d, 1, 16, 1, max_new, 0, 0)))
+    n = lib().attn_paged_workspace_bytes(_DIMS.pack(B, T, 1, H_q, H_kv, d, 1, 16, 1, max_new, 0, 0))
     if n == 0:
         raise GdnError("attn_paged_workspace_bytes", 2)
     return n
@@ -220,28 +292,23 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
     attn_paged_workspace_bytes; lse [T][H_q] float32 or None; scale defaults to d ** -0.5; no sequence has more
     than max_new new tokens."""
     torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
     B = _packed_layout(row, cu_seqlens)
     T = q.shape[0]
-    H_q = _heads_layout(_dev(q, "q", torch.bfloat16), "q", T, None, d)
-    _heads_layout(_dev(out, "out", torch.bfloat16), "out", T, H_q, d)
+    H_q = _heads_layout(q, "q", T, None, d)
+    _heads_layout(out, "out", T, H_q, d)
     if page_table is None:
         raise ValueError("page_table is required")
-    _check_cache_tensors(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
-    _ints(row, "row")
-    _ints(cu_seqlens, "cu_seqlens")
-    _contig(_dev(workspace, "workspace", torch.uint8), "workspace")
-    if lse is not None and tuple(_contig(_dev(lse, "lse", torch.float32), "lse").shape) != (T, H_q):
+    if lse is not None and lse.shape != (T, H_q):
         raise ValueError("lse must be [T][H_q]")
-    dev = _device(q, out, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, workspace, lse, k_scale, v_scale)
-    dims = AttnDims(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind)
-    cache = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(),
-                    kv_len.data_ptr())
-    with _on(dev):
-        _check("attn_paged", lib().attn_paged(
-            ctypes.byref(dims), ctypes.byref(_heads(q)), ctypes.byref(cache), row.data_ptr(), cu_seqlens.data_ptr(),
-            ctypes.byref(_heads(out)), _ptr(lse), 1.0 / math.sqrt(d) if scale is None else scale,
-            workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
+    dev = _gpu(q, "q", bf)
+    _launch("attn_paged", lib().attn_paged, dev, stream,
+            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind), _strided(q, "q", bf, dev),
+            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev), _at(row, "row", i32, dev),
+            _at(cu_seqlens, "cu_seqlens", i32, dev), _strided(out, "out", bf, dev),
+            _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
+            _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
 
 
 def kv_page_workspace_bytes(n: int, R: int, N: int) -> int:
@@ -271,93 +338,93 @@ def _pages_layout(k_pages, v_pages):
 
 
 def _lists(a, b, names):
-    _ints(a, names[0])
-    if a.dim() != 1:
-        raise ValueError(f"{names[0]} must be [n]")
-    if b is not None and _ints(b, names[1]).shape != a.shape:
-        raise ValueError(f"{names[0]} and {names[1]} must both be [n]")
+    if a.dim() != 1 or (b is not None and b.shape != a.shape):
+        raise ValueError(f"{' and '.join(names)} must be [n]")
     return a.shape[0]
 
 
-def _scratch(result, workspace):
-    if tuple(_ints(result, "result").shape) != (2,):
+def _table(page_table, kv_len, refs, dev):
+    torch = _torch()
+    i32 = torch.int32
+    return (_at(page_table, "page_table", i32, dev), _at_or_none(kv_len, "kv_len", i32, dev),
+            _at(refs, "refs", i32, dev))
+
+
+def _pools(k_pages, v_pages, dev):
+    return _at(k_pages, "k_pages", k_pages.dtype, dev), _at(v_pages, "v_pages", v_pages.dtype, dev)
+
+
+def _scratch(result, workspace, dev):
+    torch = _torch()
+    if result.shape != (2,):
         raise ValueError("result must be [2]")
-    return _contig(_dev(workspace, "workspace", _torch().uint8), "workspace")
+    return (_at(result, "result", torch.int32, dev), _at(workspace, "workspace", torch.uint8, dev),
+            workspace.numel())
 
 
 def kv_page_reserve(page_table, kv_len, refs, rows, add, result, workspace, *, page_size: int, stream=None) -> None:
     """Grow rows by add[i] tokens, with the pages for them (see ``kv_page_reserve`` in include/gdn.h).  result
     [2] int32: rows not served and the first of them or -1."""
-    R, width, N = _table_layout(_ints(page_table, "page_table"), _ints(kv_len, "kv_len"), _ints(refs, "refs"))
+    i32 = _torch().int32
+    R, width, N = _table_layout(page_table, kv_len, refs)
     n = _lists(rows, add, ("rows", "add"))
-    _scratch(result, workspace)
-    dev = _device(page_table, kv_len, refs, rows, add, result, workspace)
-    g = Pages(R, width, N, page_size, page_table.data_ptr(), kv_len.data_ptr(), refs.data_ptr())
-    with _on(dev):
-        _check("kv_page_reserve", lib().kv_page_reserve(ctypes.byref(g), rows.data_ptr(), add.data_ptr(), n,
-                                                        result.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                                        _stream(stream, dev)))
+    dev = _gpu(page_table, "page_table", i32)
+    _launch("kv_page_reserve", lib().kv_page_reserve, dev, stream,
+            _PAGES.pack(R, width, N, page_size, *_table(page_table, kv_len, refs, dev), 0, 0, 0, 0, 0, 0),
+            _at(rows, "rows", i32, dev), _at(add, "add", i32, dev), n, *_scratch(result, workspace, dev))
 
 
 def kv_page_fork(k_pages, v_pages, page_table, kv_len, refs, src_rows, dst_rows, result, workspace, *,
                  stream=None) -> None:
     """Rows dst become copies of rows src that share whole pages (see ``kv_page_fork`` in include/gdn.h).
     k_pages and v_pages may have a leading layer axis."""
+    i32 = _torch().int32
     layers, Np, page, stride, nbytes = _pages_layout(k_pages, v_pages)
-    R, width, N = _table_layout(_ints(page_table, "page_table"), _ints(kv_len, "kv_len"), _ints(refs, "refs"))
+    R, width, N = _table_layout(page_table, kv_len, refs)
     if N != Np:
         raise ValueError(f"refs counts {N} pages, the cache has {Np}")
-    _contig(_dev(k_pages, "k_pages", k_pages.dtype), "k_pages")
-    _contig(_dev(v_pages, "v_pages", v_pages.dtype), "v_pages")
     n = _lists(src_rows, dst_rows, ("src_rows", "dst_rows"))
-    _scratch(result, workspace)
-    dev = _device(k_pages, v_pages, page_table, kv_len, refs, src_rows, dst_rows, result, workspace)
-    g = Pages(R, width, N, page, page_table.data_ptr(), kv_len.data_ptr(), refs.data_ptr(), k_pages.data_ptr(),
-              v_pages.data_ptr(), layers, 0, stride, nbytes)
-    with _on(dev):
-        _check("kv_page_fork", lib().kv_page_fork(ctypes.byref(g), src_rows.data_ptr(), dst_rows.data_ptr(), n,
-                                                  result.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                                  _stream(stream, dev)))
+    dev = _gpu(page_table, "page_table", i32)
+    _launch("kv_page_fork", lib().kv_page_fork, dev, stream,
+            _PAGES.pack(R, width, N, page, *_table(page_table, kv_len, refs, dev), *_pools(k_pages, v_pages, dev),
+                        layers, 0, stride, nbytes),
+            _at(src_rows, "src_rows", i32, dev), _at(dst_rows, "dst_rows", i32, dev), n,
+            *_scratch(result, workspace, dev))
 
 
 def kv_page_free(page_table, kv_len, refs, rows, *, stream=None) -> None:
     """End rows: their pages' counts fall by one, their entries and lengths become 0 (see ``kv_page_free`` in
     include/gdn.h)."""
-    R, width, N = _table_layout(_ints(page_table, "page_table"), _ints(kv_len, "kv_len"), _ints(refs, "refs"))
+    i32 = _torch().int32
+    R, width, N = _table_layout(page_table, kv_len, refs)
     n = _lists(rows, None, ("rows",))
-    dev = _device(page_table, kv_len, refs, rows)
-    g = Pages(R, width, N, 16, page_table.data_ptr(), kv_len.data_ptr(), refs.data_ptr())
-    with _on(dev):
-        _check("kv_page_free", lib().kv_page_free(ctypes.byref(g), rows.data_ptr(), n, _stream(stream, dev)))
+    dev = _gpu(page_table, "page_table", i32)
+    _launch("kv_page_free", lib().kv_page_free, dev, stream,
+            _PAGES.pack(R, width, N, 16, *_table(page_table, kv_len, refs, dev), 0, 0, 0, 0, 0, 0),
+            _at(rows, "rows", i32, dev), n)
 
 
 def kv_page_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
     """Page src[i] to page dst[i], in every layer, k and v (see ``kv_page_copy`` in include/gdn.h)."""
+    i32 = _torch().int32
     layers, N, page, stride, nbytes = _pages_layout(k_pages, v_pages)
-    _contig(_dev(k_pages, "k_pages", k_pages.dtype), "k_pages")
-    _contig(_dev(v_pages, "v_pages", v_pages.dtype), "v_pages")
     n = _lists(src, dst, ("src", "dst"))
-    dev = _device(k_pages, v_pages, src, dst)
-    g = Pages(1, 1, N, page, None, None, None, k_pages.data_ptr(), v_pages.data_ptr(), layers, 0, stride, nbytes)
-    with _on(dev):
-        _check("kv_page_copy", lib().kv_page_copy(ctypes.byref(g), src.data_ptr(), dst.data_ptr(), n,
-                                                  _stream(stream, dev)))
+    dev = _gpu(src, "src", i32)
+    _launch("kv_page_copy", lib().kv_page_copy, dev, stream,
+            _PAGES.pack(1, 1, N, page, 0, 0, 0, *_pools(k_pages, v_pages, dev), layers, 0, stride, nbytes),
+            _at(src, "src", i32, dev), _at(dst, "dst", i32, dev), n)
 
 
 def kv_page_compact(k_pages, v_pages, page_table, refs, remap, result, workspace, *, stream=None) -> None:
     """Move the pages in use to the pool's low numbers (see ``kv_page_compact`` in include/gdn.h).  remap [N]
     int32 gets each page's new number (0: free), result [2] the pages in use and how many moved."""
+    i32 = _torch().int32
     layers, Np, page, stride, nbytes = _pages_layout(k_pages, v_pages)
-    R, width, N = _table_layout(_ints(page_table, "page_table"), None, _ints(refs, "refs"))
-    if N != Np or tuple(_ints(remap, "remap").shape) != (N,):
+    R, width, N = _table_layout(page_table, None, refs)
+    if N != Np or remap.shape != (N,):
         raise ValueError(f"refs and remap must be [{Np}] as the cache has pages")
-    _contig(_dev(k_pages, "k_pages", k_pages.dtype), "k_pages")
-    _contig(_dev(v_pages, "v_pages", v_pages.dtype), "v_pages")
-    _scratch(result, workspace)
-    dev = _device(k_pages, v_pages, page_table, refs, remap, result, workspace)
-    g = Pages(R, width, N, page, page_table.data_ptr(), None, refs.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-              layers, 0, stride, nbytes)
-    with _on(dev):
-        _check("kv_page_compact", lib().kv_page_compact(ctypes.byref(g), remap.data_ptr(), result.data_ptr(),
-                                                        workspace.data_ptr(), workspace.numel(),
-                                                        _stream(stream, dev)))
+    dev = _gpu(page_table, "page_table", i32)
+    _launch("kv_page_compact", lib().kv_page_compact, dev, stream,
+            _PAGES.pack(R, width, N, page, *_table(page_table, None, refs, dev), *_pools(k_pages, v_pages, dev),
+                        layers, 0, stride, nbytes),
+            _at(remap, "remap", i32, dev), *_scratch(result, workspace, dev))

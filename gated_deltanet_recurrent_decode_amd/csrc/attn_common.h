@@ -80,6 +80,59 @@ __device__ __forceinline__ Seq read_seq(const AttnParams &p, int b)
     return s;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    if (((unsigned long long)a | (unsigned long long)b) >> 32)
+        return (long long)((unsigned long long)a / (unsigned long long)b);
+    return (uint32_t)a / (uint32_t)b;
+}
+
+// Work in units on one line, cut into pieces, one a workgroup, none of them empty; piece w
+// begins at unit piece_begin(w).
+__device__ __forceinline__ int pieces_of(const AttnParams &p, long long total)
+{
+    return total < p.workgroups ? (int)total : p.workgroups;
+}
+
+__device__ __forceinline__ long long piece_begin(long long total, int w, int pieces)
+{
+    return total == pieces ? w : quotient(total * w, pieces);
+}
+
+// The piece that holds unit u: the last w with piece_begin(w) <= u.
+__device__ __forceinline__ int owner_of(long long total, long long u, int pieces)
+{
+    return total == pieces ? (int)u : (int)quotient((u + 1) * pieces - 1, total);
+}
+
+// A (sequence, kv head, tile) that begins in a workgroup's piece and goes on behind it: what
+// the join needs of it, left in the workspace by that workgroup.
+struct Cut {
+    int last;  // piece of its last unit; -1: there is none
+    int slot;  // its part in this workgroup's piece, 0 or 1 (0 in the pieces behind)
+    int first; // its sequence's first token
+    int rows;  // its sequence's rows
+    int h, tile;
+};
+
+__device__ __forceinline__ void write_cut(const AttnParams &p, int w, const Cut &c)
+{
+    int32_t *o = p.cut + (int64_t)w * 8;
+    o[0] = c.last;
+    o[1] = c.slot;
+    o[2] = c.first;
+    o[3] = c.rows;
+    o[4] = c.h;
+    o[5] = c.tile;
+}
+
+__device__ __forceinline__ Cut read_cut(const AttnParams &p, int w)
+{
+    const int32_t *o = p.cut + (int64_t)w * 8;
+    return Cut{o[0], o[1], o[2], o[3], o[4], o[5]};
+}
+
 // log2 of a sum relative to a maximum, as a natural logarithm
 __device__ __forceinline__ float lse_of(float m, float l)
 {

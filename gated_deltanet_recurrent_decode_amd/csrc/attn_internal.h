@@ -31,6 +31,7 @@ struct AttnParams {
     const int32_t *page_table, *kv_len, *row, *cu;
     float *part_o;              // partial outputs [workgroups][2][rows of a tile][d]
     float *part_ml;             // their running maximum and sum [workgroups][2][rows of a tile][2]
+    int32_t *cut;               // [workgroups][8] what of the workgroup's piece goes on in the next, see Cut
     float scale;                // in the exponent of 2
     int B, T, R, H_q, H_kv, G, N, page_shift, width, max_new, window;
     int workgroups;

@@ -54,26 +54,26 @@ __device__ __forceinline__ long long seq_units(const AttnParams &p, const RowSeq
 }
 
 struct Place {
-    int b;          // sequence
+    int b;            // sequence, -1: nowhere
     long long before; // units before it
     long long total;  // units of the call
+    RowSeq s;
 };
 
 // Where the line of units holds what `hit` asks for (a predicate of a sequence,
-// its first unit and the units of the call), and the units of the call.  b = -1 if nowhere.
-template <class Hit>
-__device__ Place locate(const AttnParams &p, Hit hit)
+// its first unit, its units and the units of the call).  TH threads.
+template <int TH, class Hit>
+__device__ __forceinline__ Place locate(const AttnParams &p, Hit hit)
 {
-    __shared__ long long wave_sum[4];
-    __shared__ long long found_before;
-    __shared__ int found;
+    __shared__ long long wave_sum[TH / 64];
+    __shared__ Place found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     long long total = 0;
     if (tid == 0)
-        found = -1;
+        found.b = -1;
     for (int pass = 0; pass < 2; ++pass) {
         long long run = 0;
-        for (int b0 = 0; b0 < p.B; b0 += NT) {
+        for (int b0 = 0; b0 < p.B; b0 += TH) {
             const int b = b0 + tid;
             RowSeq s;
             long long u = 0;
@@ -93,43 +93,25 @@ __device__ Place locate(const AttnParams &p, Hit hit)
                 wave_sum[wave] = inc;
             __syncthreads();
             long long before = run;
-            for (int w = 0; w < 4; ++w) {
+#pragma unroll
+            for (int w = 0; w < TH / 64; ++w) {
                 if (w < wave)
                     before += wave_sum[w];
                 run += wave_sum[w];
             }
-            if (pass == 1 || p.B <= NT) {
-                if (u > 0 && hit(s, before + inc - u, u, p.B <= NT ? run : total)) {
-                    found = b;
-                    found_before = before + inc - u;
-                }
+            if (pass == 1 || p.B <= TH) {
+                const long long all = p.B <= TH ? run : total;
+                if (u > 0 && hit(s, before + inc - u, u, all))
+                    found = Place{b, before + inc - u, all, s};
             }
         }
         if (pass == 0)
             total = run;
-        if (p.B <= NT)
+        if (p.B <= TH)
             break;
     }
     __syncthreads();
-    Place at;
-    at.b = found;
-    at.before = found_before;
-    at.total = total;
-    return at;
-}
-
-// Pieces of the line, one a workgroup, none of them empty; piece w begins at unit piece(w).
-__device__ __forceinline__ int pieces_of(const AttnParams &p, long long total)
-{
-    return total < p.workgroups ? (int)total : p.workgroups;
-}
-
-__device__ __forceinline__ long long piece(long long total, int w, int pieces) { return total * w / pieces; }
-
-// The piece that holds unit u: the last w with piece(w) <= u.
-__device__ __forceinline__ int owner_of(long long total, long long u, int pieces)
-{
-    return (int)(((u + 1) * pieces - 1) / total);
+    return found;
 }
 
 } // namespace
@@ -148,37 +130,41 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
     const int n_ = lane & 15, g = lane >> 4;
     const int w = blockIdx.x;
 
-    const Place at = locate(p, [&](const RowSeq &, long long before, long long units, long long total) {
+    const Place at = locate<NT>(p, [&](const RowSeq &, long long before, long long units, long long total) {
         const int pieces = pieces_of(p, total);
-        const long long u0 = piece(total, w, pieces);
+        const long long u0 = piece_begin(total, w, pieces);
         return w < pieces && before <= u0 && u0 < before + units;
     });
+    if (tid == 0)
+        write_cut(p, w, Cut{-1});
     if (at.b < 0)
         return;
     const int pieces = pieces_of(p, at.total);
-    long long u = piece(at.total, w, pieces);
-    const long long u_end = piece(at.total, w + 1, pieces);
+    long long u = piece_begin(at.total, w, pieces);
+    const long long u_end = piece_begin(at.total, w + 1, pieces);
     const long long u_begin = u;
     int b = at.b;
     long long before = at.before;
+    RowSeq s = at.s;
 
     while (u < u_end) {
-        const RowSeq s = read_row_seq(p, b);
         const long long units = seq_units(p, s);
         if (u >= before + units) {
             before += units;
-            ++b;
+            s = read_row_seq(p, ++b);
             continue;
         }
         const long long v = u - before;
-        const long long ht = v / s.units;
+        const long long ht = quotient(v, s.units);
         const int unit0 = (int)(v - ht * s.units);
-        const int tile = (int)(ht % s.tiles), h = (int)(ht / s.tiles);
+        const int h = (int)quotient(ht, s.tiles), tile = (int)(ht - (long long)h * s.tiles);
         const long long t0 = before + ht * s.units, t1 = t0 + s.units;
         const long long e = t1 < u_end ? t1 : u_end;
         const int unit1 = unit0 + (int)(e - u);
         const bool whole = u == t0 && e == t1;
         const int slot = u == u_begin ? 0 : 1;
+        if (tid == 0 && u == t0 && e < t1)
+            write_cut(p, w, Cut{owner_of(at.total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, tile});
         u = e;
 
         // this lane's row: a token and a head of the group
@@ -462,71 +448,103 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
     }
 }
 
-// The rows whose keys were cut into pieces: their parts' (o, m, l) together, in
-// the order of the pieces.  A workgroup a token and kv head, a wave a row.
+// The rows whose keys were cut into pieces: their parts' (o, m, l) together, in a
+// fixed order.  blockIdx = the piece they begin in and the row of the tile; eight
+// waves take every eighth part, four at a time with their sums, and meet in LDS.
+constexpr int JT = 512;
 template <int D, bool E4M3>
-__global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams p)
+__global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
 {
-    constexpr int E = D / 64;
-    const int t = blockIdx.x, h = blockIdx.y;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Place at = locate(p, [&](const RowSeq &s, long long, long long, long long) {
-        return t >= s.first && t < s.first + s.n;
-    });
-    if (at.b < 0)
+    constexpr int E = D / 64, JW = JT / 64, BATCH = 4;
+    __shared__ float sm_m[JW], sm_l[JW], sm_o[JW][D];
+    const int w0 = blockIdx.x, rr = blockIdx.y;
+    const Cut c = read_cut(p, w0);
+    const int row = c.tile * TM + rr;
+    if (c.last < 0 || row >= c.rows)
         return;
-    const RowSeq s = read_row_seq(p, at.b);
-    const int pieces = pieces_of(p, at.total);
-    for (int q = wave; q < p.G; q += 4) {
-        const int row = (t - s.first) * p.G + q;
-        const int tile = row / TM, rr = row % TM;
-        const long long u0 = at.before + ((long long)h * s.tiles + tile) * s.units, u1 = u0 + s.units;
-        const int w0 = owner_of(at.total, u0, pieces);
-        int w1 = owner_of(at.total, u1 - 1, pieces);
-        w1 = w1 < pieces ? w1 : pieces - 1;
-        if (w0 == w1)
-            continue; // finished where it was computed
-        const int slot0 = piece(at.total, w0, pieces) == u0 ? 0 : 1;
-        float m = neg_inf();
-        for (int w = w0 + lane; w <= w1; w += 64)
-            m = fmaxf(m, p.part_ml[(((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TM + rr) * 2]);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int w1 = c.last < p.workgroups ? c.last : p.workgroups - 1, slot0 = c.slot, h = c.h;
+    const int64_t t = c.first + row / p.G;
+    const int hq = h * p.G + row % p.G;
+    float m = neg_inf(), l = 0.f, o[E];
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1)
-            m = fmaxf(m, __shfl_xor(m, x));
-        const float m_safe = m == neg_inf() ? 0.f : m;
-        float l = 0.f, o[E];
+    for (int i = 0; i < E; ++i)
+        o[i] = 0.f;
+    for (int w = w0 + wave; w <= w1; w += JW * BATCH) {
+        float pm[BATCH], pl[BATCH], po[BATCH][E];
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            o[i] = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-            const int64_t part = ((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TM + rr;
-            const float f = __builtin_amdgcn_exp2f(p.part_ml[part * 2] - m_safe);
-            l = fmaf(p.part_ml[part * 2 + 1], f, l);
+        for (int k = 0; k < BATCH; ++k) {
+            const int wk = w + k * JW <= w1 ? w + k * JW : w;
+            const int64_t part = ((int64_t)wk * 2 + (wk == w0 ? slot0 : 0)) * TM + rr;
+            pm[k] = p.part_ml[part * 2];
+            pl[k] = p.part_ml[part * 2 + 1];
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                o[i] = fmaf(p.part_o[part * D + i * 64 + lane], f, o[i]);
+                po[k][i] = p.part_o[part * D + i * 64 + lane];
         }
-        const int hq = h * p.G + q;
-        const float vs = E4M3 ? p.v_scale[h] : 1.0f;
-        const float inv = l == 0.f ? 0.f : vs / l;
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            top = fmaxf(top, pm[k]);
+        const float safe = top == neg_inf() ? 0.f : top;
+        const float keep = __builtin_amdgcn_exp2f(m - safe);
+        l *= keep;
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            p.out.p[(int64_t)t * p.out.row + (int64_t)hq * p.out.head + i * 64 + lane] = f32_to_bf16_rne(o[i] * inv);
-        if (lane == 0 && p.lse)
-            p.lse[(int64_t)t * p.H_q + hq] = lse_of(m, l);
+            o[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            if (w + k * JW <= w1) { // uniform
+                const float f = __builtin_amdgcn_exp2f(pm[k] - safe);
+                l = fmaf(pl[k], f, l);
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    o[i] = fmaf(po[k][i], f, o[i]);
+            }
+        }
+        m = top;
+    }
+    if (lane == 0) {
+        sm_m[wave] = m;
+        sm_l[wave] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        sm_o[wave][i * 64 + lane] = o[i];
+    __syncthreads();
+    if (tid < D) {
+        float top = neg_inf();
+#pragma unroll
+        for (int k = 0; k < JW; ++k)
+            top = fmaxf(top, sm_m[k]);
+        const float safe = top == neg_inf() ? 0.f : top;
+        float sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int k = 0; k < JW; ++k) {
+            const float f = __builtin_amdgcn_exp2f(sm_m[k] - safe);
+            sum = fmaf(sm_l[k], f, sum);
+            x = fmaf(sm_o[k][tid], f, x);
+        }
+        const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+        const float inv = sum == 0.f ? 0.f : vs / sum;
+        p.out.p[t * p.out.row + (int64_t)hq * p.out.head + tid] = f32_to_bf16_rne(x * inv);
+        if (tid == 0 && p.lse)
+            p.lse[t * p.H_q + hq] = lse_of(top, sum);
     }
 }
 
 size_t attn_rows_layout(int d, void *base, AttnParams *p)
 {
     const int workgroups = 2 * device_cus();
-    const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4);
+    const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4),
+                 cut = round256((size_t)workgroups * 8 * 4);
     if (p) {
         p->workgroups = workgroups;
         p->part_o = static_cast<float *>(base);
         p->part_ml = reinterpret_cast<float *>(static_cast<char *>(base) + o);
+        p->cut = reinterpret_cast<int32_t *>(static_cast<char *>(base) + o + ml);
     }
-    return o + ml;
+    return o + ml + cut;
 }
 
 template <int D, bool E4M3>
@@ -538,7 +556,8 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
                                    dim3((unsigned)p.workgroups), dim3(NT), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_join_kernel<D, E4M3>),
-                            dim3((unsigned)p.T, (unsigned)p.H_kv), dim3(NT), args, 0, stream);
+                            dim3((unsigned)p.workgroups, (unsigned)(p.max_new * p.G < TM ? p.max_new * p.G : TM)),
+                            dim3(JT), args, 0, stream);
     return e;
 }
 

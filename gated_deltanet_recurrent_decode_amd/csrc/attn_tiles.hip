@@ -64,18 +64,6 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s)
     return s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TR - 1) / TR);
 }
 
-__device__ __forceinline__ int pieces_of(const AttnParams &p, long long total)
-{
-    return total < p.workgroups ? (int)total : p.workgroups;
-}
-
-__device__ __forceinline__ long long piece(long long total, int w, int pieces) { return total * w / pieces; }
-
-__device__ __forceinline__ int owner_of(long long total, long long u, int pieces)
-{
-    return (int)(((u + 1) * pieces - 1) / total);
-}
-
 // The entry that holds unit u (before[e] <= u < before[e + 1]): 64 probes a round.
 __device__ __forceinline__ int entry_of(const long long *before, int count, long long u)
 {
@@ -205,16 +193,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     const int n_ = lane & 31, hh = lane >> 5;
     const int count = *p.count;
     const long long total = p.before[count];
-    if (total == 0)
-        return;
-    const int pieces = pieces_of(p, total);
     // consecutive pieces on one XCD (workgroups go round the eight): they share keys in its L2
-    const int per = (p.workgroups + 7) / 8;
+    const int per = p.workgroups / 8;
     const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (tid == 0)
+        write_cut(p, w, Cut{-1});
+    const int pieces = pieces_of(p, total);
     if (w >= pieces)
         return;
-    long long u = piece(total, w, pieces);
-    const long long u_begin = u, u_end = piece(total, w + 1, pieces);
+    long long u = piece_begin(total, w, pieces);
+    const long long u_begin = u, u_end = piece_begin(total, w + 1, pieces);
     int e = uniform(entry_of(p.before, count, u));
 
     // a 16-byte chunk's place within its row
@@ -242,6 +230,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
         const int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
         const bool whole = u == t0 && stop == t1;
         const int slot = u == u_begin ? 0 : 1;
+        if (tid == 0 && u == t0 && stop < t1)
+            write_cut(p, w, Cut{owner_of(total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, tile});
         u = stop;
         ++e;
 
@@ -587,56 +577,60 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     }
 }
 
-// blockIdx.x = a piece: the entry that begins in it and goes on in the next; a wave a row of it.
+// blockIdx.x = a piece: what begins in it and goes on in the next; a wave a row of it.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void attn_tiles_join_kernel(AttnParams p)
 {
-    constexpr int E = D / 64;
+    constexpr int E = D / 64, BATCH = 2;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int count = *p.count;
-    const long long total = p.before[count];
     const int w0 = blockIdx.x;
-    if (total == 0)
+    const Cut c = read_cut(p, w0);
+    if (c.last < 0)
         return;
-    const int pieces = pieces_of(p, total);
-    if (w0 + 1 >= pieces)
-        return;
-    const long long begin = piece(total, w0, pieces), next = piece(total, w0 + 1, pieces);
-    const int e = uniform(entry_of(p.before, count, next - 1));
-    const long long u0 = p.before[e], u1 = p.before[e + 1];
-    if (u0 < begin || u1 <= next)
-        return; // begun in an earlier piece, or whole
-    int w1 = owner_of(total, u1 - 1, pieces);
-    w1 = w1 < pieces ? w1 : pieces - 1;
-    const int slot0 = u0 == begin ? 0 : 1;
-    const Seq s = read_seq(p, p.entry[(int64_t)e * 3]);
-    const int h = p.entry[(int64_t)e * 3 + 1], tile = p.entry[(int64_t)e * 3 + 2];
-    const int rows = s.n * p.G;
+    const int w1 = c.last < p.workgroups ? c.last : p.workgroups - 1, slot0 = c.slot, h = c.h;
     for (int rr = blockIdx.y * 4 + wave; rr < TR; rr += gridDim.y * 4) {
-        const int row = tile * TR + rr;
-        if (row >= rows)
+        const int row = c.tile * TR + rr;
+        if (row >= c.rows)
             break;
         auto part_of = [&](int w) { return ((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TR + rr; };
-        float m = neg_inf();
-        for (int w = w0 + lane; w <= w1; w += 64)
-            m = fmaxf(m, p.part_ml[part_of(w) * 2]);
-#pragma unroll
-        for (int x = 1; x < 64; x <<= 1)
-            m = fmaxf(m, __shfl_xor(m, x));
-        const float m_safe = m == neg_inf() ? 0.f : m;
-        float l = 0.f, o[E];
+        float m = neg_inf(), l = 0.f, o[E];
 #pragma unroll
         for (int i = 0; i < E; ++i)
             o[i] = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-            const int64_t part = part_of(w);
-            const float f = __builtin_amdgcn_exp2f(p.part_ml[part * 2] - m_safe);
-            l = fmaf(p.part_ml[part * 2 + 1], f, l);
+        for (int w = w0; w <= w1; w += BATCH) {
+            float pm[BATCH], pl[BATCH], po[BATCH][E];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int64_t part = part_of(w + k <= w1 ? w + k : w);
+                pm[k] = p.part_ml[part * 2];
+                pl[k] = p.part_ml[part * 2 + 1];
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    po[k][i] = p.part_o[part * D + i * 64 + lane];
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                top = fmaxf(top, pm[k]);
+            const float safe = top == neg_inf() ? 0.f : top;
+            const float keep = __builtin_amdgcn_exp2f(m - safe);
+            l *= keep;
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                o[i] = fmaf(p.part_o[part * D + i * 64 + lane], f, o[i]);
+                o[i] *= keep;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (w + k <= w1) {
+                    const float f = __builtin_amdgcn_exp2f(pm[k] - safe);
+                    l = fmaf(pl[k], f, l);
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        o[i] = fmaf(po[k][i], f, o[i]);
+                }
+            }
+            m = top;
         }
-        const int64_t t = s.first + row / p.G;
+        const int64_t t = c.first + row / p.G;
         const int hq = h * p.G + row % p.G;
         const float vs = E4M3 ? p.v_scale[h] : 1.0f;
         const float inv = l == 0.f ? 0.f : vs / l;
@@ -653,7 +647,8 @@ size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnP
     const int workgroups = (device_cus() + 7) / 8 * 8;
     const size_t entries = ((size_t)T * G / TR + B) * H_kv;
     const size_t o = round256((size_t)workgroups * 2 * TR * d * 4), ml = round256((size_t)workgroups * 2 * TR * 2 * 4),
-                 bf = round256((entries + 1) * 8), en = round256(entries * 3 * 4);
+                 bf = round256((entries + 1) * 8), en = round256(entries * 3 * 4),
+                 cut = round256((size_t)workgroups * 8 * 4);
     if (p) {
         char *at = static_cast<char *>(base);
         p->workgroups = workgroups;
@@ -661,9 +656,10 @@ size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnP
         p->part_ml = reinterpret_cast<float *>(at + o);
         p->before = reinterpret_cast<long long *>(at + o + ml);
         p->entry = reinterpret_cast<int32_t *>(at + o + ml + bf);
-        p->count = reinterpret_cast<int32_t *>(at + o + ml + bf + en);
+        p->cut = reinterpret_cast<int32_t *>(at + o + ml + bf + en);
+        p->count = reinterpret_cast<int32_t *>(at + o + ml + bf + en + cut);
     }
-    return o + ml + bf + en + 256;
+    return o + ml + bf + en + cut + 256;
 }
 
 template <int D, bool E4M3>
@@ -680,7 +676,7 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
                             dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_join_kernel<D, E4M3>),
-                            dim3((unsigned)p.workgroups, 16), dim3(256), args, 0, stream);
+                            dim3((unsigned)p.workgroups, 32), dim3(256), args, 0, stream);
     return e;
 }
 
