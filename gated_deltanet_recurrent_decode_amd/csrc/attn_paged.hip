@@ -457,24 +457,30 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
 {
     constexpr int E = D / 64, JW = JT / 64, BATCH = 4;
     __shared__ float sm_m[JW], sm_l[JW], sm_o[JW][D];
-    const int w0 = blockIdx.x, rr = blockIdx.y;
+    const int w0 = blockIdx.x;
     const Cut c = read_cut(p, w0);
-    const int row = c.tile * TM + rr;
-    if (c.last < 0 || row >= c.rows)
+    if (c.last < 0)
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int w1 = c.last < p.workgroups ? c.last : p.workgroups - 1, slot0 = c.slot, h = c.h;
+    // few parts: a wave a row, eight rows a workgroup; many: eight waves a row
+    const bool alone = w1 - w0 < BATCH;
+    const int rr = alone ? blockIdx.y * JW + wave : blockIdx.y;
+    const int step = alone ? 1 : JW;
+    const int row = c.tile * TM + rr;
+    if (rr >= TM || row >= c.rows)
+        return; // alone: each wave for itself, with no barrier behind
     const int64_t t = c.first + row / p.G;
     const int hq = h * p.G + row % p.G;
     float m = neg_inf(), l = 0.f, o[E];
 #pragma unroll
     for (int i = 0; i < E; ++i)
         o[i] = 0.f;
-    for (int w = w0 + wave; w <= w1; w += JW * BATCH) {
+    for (int w = alone ? w0 : w0 + wave; w <= w1; w += step * BATCH) {
         float pm[BATCH], pl[BATCH], po[BATCH][E];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int wk = w + k * JW <= w1 ? w + k * JW : w;
+            const int wk = w + k * step <= w1 ? w + k * step : w;
             const int64_t part = ((int64_t)wk * 2 + (wk == w0 ? slot0 : 0)) * TM + rr;
             pm[k] = p.part_ml[part * 2];
             pl[k] = p.part_ml[part * 2 + 1];
@@ -494,7 +500,7 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
             o[i] *= keep;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if (w + k * JW <= w1) { // uniform
+            if (w + k * step <= w1) { // uniform
                 const float f = __builtin_amdgcn_exp2f(pm[k] - safe);
                 l = fmaf(pl[k], f, l);
 #pragma unroll
@@ -503,6 +509,16 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
             }
         }
         m = top;
+    }
+    const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+    if (alone) {
+        const float inv = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            p.out.p[t * p.out.row + (int64_t)hq * p.out.head + i * 64 + lane] = f32_to_bf16_rne(o[i] * inv);
+        if (lane == 0 && p.lse)
+            p.lse[t * p.H_q + hq] = lse_of(m, l);
+        return;
     }
     if (lane == 0) {
         sm_m[wave] = m;
@@ -525,7 +541,6 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
             sum = fmaf(sm_l[k], f, sum);
             x = fmaf(sm_o[k][tid], f, x);
         }
-        const float vs = E4M3 ? p.v_scale[h] : 1.0f;
         const float inv = sum == 0.f ? 0.f : vs / sum;
         p.out.p[t * p.out.row + (int64_t)hq * p.out.head + tid] = f32_to_bf16_rne(x * inv);
         if (tid == 0 && p.lse)

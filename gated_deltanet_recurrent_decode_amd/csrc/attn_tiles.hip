@@ -179,14 +179,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     constexpr int CH = D / 8;                 // chunks of a row
     constexpr int ST = D / 16;                // steps of a score's contraction
     constexpr int DT = D / 32;                // 32-column tiles of o
-    constexpr int SUB = D == 256 ? 32 : 64;   // keys between two softmax steps: registers allow no more
-    constexpr int NS = SUB / 32;
     constexpr int ROWB = D * 2;               // bytes of an LDS row
     constexpr int KB = block_keys(D);
+    constexpr int NS = KB / 32;
     // steps whose queries a lane keeps in LDS, each lane its own: all 16 of 256 columns in
     // registers, beside 128 of o, spill
     constexpr int QL = D == 256 ? 8 : 0;
     __shared__ __align__(16) uint8_t sm_k[2][KB * ROWB], sm_v[2][KB * ROWB];
+    __shared__ int sm_odd[2];
     __shared__ u32x4 sm_q[QL ? NW * RS * QL * 64 : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -352,6 +352,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
 
         const int end = span.hi > span.lo ? blk1 : blk0; // no keys: nothing to walk
         __syncthreads(); // the buffers of the piece before are read
+        if (tid < 2)
+            sm_odd[tid] = 0;
         if (blk0 < end) {
             find_missing(span.lo + blk0 * KB);
             if constexpr (E4M3) {
@@ -373,6 +375,34 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                 else
                     stage(key0 + KB, buf ^ 1);
             }
+            // A block that some row does not see whole: v of keys past the sequence's last is cleared,
+            // and so are infinities and NaN, which 0 times would carry into rows that do not see them.
+            bool odd = false;
+            if (key0 + KB - 1 > span.min_pos || (p.window > 0 && key0 <= span.max_pos - p.window)) {
+                if (tid == 0)
+                    sm_odd[buf ^ 1] = 0;
+#pragma unroll
+                for (int q = 0; q < KB * CH / NT; ++q) {
+                    const int x = tid + q * NT, key = key0 + x / CH;
+                    u32x4 *at = reinterpret_cast<u32x4 *>(&sm_v[buf][x * 16]);
+                    u32x4 v = *at;
+                    bool found = false;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const bool lo_odd = (v[y] & 0x7f80u) == 0x7f80u, hi_odd = (v[y] & 0x7f800000u) == 0x7f800000u;
+                        found |= lo_odd | hi_odd;
+                        v[y] &= (lo_odd ? 0xffff0000u : 0xffffffffu) & (hi_odd ? 0xffffu : 0xffffffffu);
+                    }
+                    if (key >= s.L)
+                        *at = u32x4{0u, 0u, 0u, 0u};
+                    else if (found) {
+                        *at = v;
+                        sm_odd[buf] = 1;
+                    }
+                }
+                __syncthreads();
+                odd = sm_odd[buf] != 0;
+            }
             if (any && key0 <= max_pos && !(p.window > 0 && key0 + KB - 1 <= min_pos - p.window)) {
                 if (lost) {
 #pragma unroll
@@ -385,9 +415,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                 int k_at = k_chunk, v_at[2] = {v_base[0], v_base[1]};
                 asm volatile("" : "+v"(k_at), "+v"(v_at[0]), "+v"(v_at[1]));
                 const bool mixed = key0 + KB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
-#pragma unroll
-                for (int part = 0; part < KB / SUB; ++part) {
-                    const uint8_t *kb = sm_k[buf] + part * SUB * ROWB, *vb = sm_v[buf] + part * SUB * ROWB;
+                const uint8_t *kb = sm_k[buf], *vb = sm_v[buf];
+                {
                     f32x16 sc[RS][NS];
 #pragma unroll
                     for (int x = 0; x < RS; ++x)
@@ -426,7 +455,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
                                     const int back =
-                                        pos[x] - (key0 + part * SUB + y * 32 + 8 * (i >> 2) + 4 * hh + (i & 3));
+                                        pos[x] - (key0 + y * 32 + 8 * (i >> 2) + 4 * hh + (i & 3));
                                     if (back < 0 || back > reach)
                                         sc[x][y][i] = neg_inf();
                                 }
@@ -477,7 +506,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                         }
                         l[x] += sum;
                     }
-                    bool odd = false;
 #pragma unroll
                     for (int q = 0; q < 2 * NS; ++q)
 #pragma unroll
@@ -493,36 +521,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                                 vf[2 * y] = v2[0];
                                 vf[2 * y + 1] = v2[1];
                             }
-                            if (mixed) {
-                                // infinities and NaN must not reach rows that do not see their key:
-                                // out of the product, into the rows that do below
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const bool lo_odd = (vf[y] & 0x7f80u) == 0x7f80u;
-                                    const bool hi_odd = (vf[y] & 0x7f800000u) == 0x7f800000u;
-                                    odd |= lo_odd | hi_odd;
-                                    vf[y] &= (lo_odd ? 0xffff0000u : 0xffffffffu) & (hi_odd ? 0xffffu : 0xffffffffu);
-                                }
-                            }
 #pragma unroll
                             for (int x = 0; x < RS; ++x)
                                 acc[x][a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf),
                                                                                     pf[x][q], acc[x][a], 0, 0, 0);
                         }
-                    if (mixed && __ballot(odd)) {
-                        for (int j = 0; j < SUB; ++j) {
+                    if (odd) { // uniform: what left the product goes to the rows that see it
+                        for (int j = 0; j < KB && key0 + j < s.L; ++j) {
+                            const int64_t cell = cell_of(key0 + j) * D;
 #pragma unroll
                             for (int a = 0; a < DT; ++a)
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
-                                    const int col = a * 32 + 8 * (i >> 2) + 4 * hh + (i & 3);
-                                    const uint32_t y =
-                                        (uint32_t) * reinterpret_cast<const uint16_t *>(
-                                                         vb + j * ROWB + ((col >> 3) ^ swizzle(j)) * 16 + (col & 7) * 2)
-                                        << 16;
+                                    const int64_t at = cell + a * 32 + 8 * (i >> 2) + 4 * hh + (i & 3);
+                                    uint32_t y;
+                                    if constexpr (E4M3)
+                                        y = e4m3_to_bf16<false>(static_cast<const uint8_t *>(p.v_pages)[at]) << 16;
+                                    else
+                                        y = (uint32_t) static_cast<const uint16_t *>(p.v_pages)[at] << 16;
 #pragma unroll
                                     for (int x = 0; x < RS; ++x) {
-                                        const int back = pos[x] - (key0 + part * SUB + j);
+                                        const int back = pos[x] - (key0 + j);
                                         if (back >= 0 && back <= reach && (y & 0x7f800000u) == 0x7f800000u)
                                             acc[x][a][i] += __uint_as_float(y);
                                     }
