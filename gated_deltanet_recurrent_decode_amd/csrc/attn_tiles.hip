@@ -35,8 +35,6 @@ constexpr int PT = 1024; // the planning workgroup
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint32_t lds_u32;
-typedef __attribute__((address_space(1))) const uint32_t global_u32;
 
 // What a tile of a sequence sees: keys lo .. hi - 1, in blocks from lo on.
 struct Span {
@@ -62,6 +60,18 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int t
 __device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s)
 {
     return s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TR - 1) / TR);
+}
+
+// 16 bytes a lane from base + off into LDS, lane after lane from `to` on.  As inline assembly
+// because the compiler, given the builtin, waits for it before any read of LDS: the loads of the
+// next block would be waited for before this one is worked on.  Whoever reads `to` waits for
+// vmcnt(0) and a barrier first.
+__device__ __forceinline__ void load_to_lds(uint8_t *to, const uint8_t *base, int off)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)at)), "v"(off),
+                 "s"(base)
+                 : "memory", "m0");
 }
 
 // The entry that holds unit u (before[e] <= u < before[e + 1]): 64 probes a round.
@@ -174,7 +184,7 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
 template <int D, bool E4M3, int NW, int RS>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams p)
 {
-    static_assert(NW * RS * 32 == TR, "a workgroup's rows");
+    static_assert(NW * RS * 32 == TR && RS == 1, "a workgroup's rows");
     constexpr int NT = 64 * NW;
     constexpr int CH = D / 8;                 // chunks of a row
     constexpr int ST = D / 16;                // steps of a score's contraction
@@ -182,11 +192,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     constexpr int ROWB = D * 2;               // bytes of an LDS row
     constexpr int KB = block_keys(D);
     constexpr int NS = KB / 32;
+    constexpr int KA = D == 256 ? (E4M3 ? 1 : 2) : 4; // products whose LDS reads go ahead together
     // steps whose queries a lane keeps in LDS, each lane its own: all 16 of 256 columns in
     // registers, beside 128 of o, spill
-    constexpr int QL = D == 256 ? 8 : 0;
+    constexpr int QL = D == 256 ? 11 : 0;
     __shared__ __align__(16) uint8_t sm_k[2][KB * ROWB], sm_v[2][KB * ROWB];
     __shared__ int sm_odd[2];
+    __shared__ __align__(4) uint8_t sm_lost[2][4]; // a block's 16-key parts whose page is outside the pool
     __shared__ u32x4 sm_q[QL ? NW * RS * QL * 64 : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -288,92 +300,94 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
             const int pg = key < s.L ? tab[key >> p.page_shift] : 0;
             return pg < 1 || pg >= p.N ? 0 : pg;
         };
-        // which of a block's 16-key parts hold keys on a page outside the pool
-        int missing = 0;
-        auto find_missing = [&](int key0) {
-            missing = 0;
-#pragma unroll
-            for (int q = 0; q < KB / 16; ++q)
-                if (key0 + 16 * q < s.L && page_of(key0 + 16 * q) == 0)
-                    missing |= 1 << q;
-        };
         auto cell_of = [&](int key) {
             return (((int64_t)page_of(key) * p.H_kv + h) << p.page_shift) + (key & inside);
         };
-        // bf16: k and v of a block into LDS, one 1 KiB instruction at a time
-        constexpr int PER = KB * CH / 64 / NW; // of each array, a wave
-        constexpr int RP = 64 / CH;            // rows of an instruction
-        static_assert(PER * NW * RP == KB, "every row of a block is staged once");
-        auto stage = [&](int key0, int buf) {
+        // Staging: a wave brings the same few rows of every block, all of them on one page.  Its
+        // number is read a block ahead, by the scalar unit.
+        constexpr int WR = E4M3 ? 1024 / D : KB / NW; // rows of a wave
+        const int my_row = wave * WR;
+        auto *table = (__attribute__((address_space(4))) const int32_t *)tab;
+        auto next_page = [&](int key0) {
+            const int key = uniform(key0 + my_row);
+            return my_row < KB && key < s.L ? table[key >> p.page_shift] : 0;
+        };
+        auto first_cell = [&](int key0, int buf, int id) { // of the wave's rows
+            const bool ok = id > 0 && id < p.N;
+            if (lane == 0 && my_row < KB)
+                sm_lost[buf][my_row >> 4] = !ok && key0 + my_row < s.L;
+            return ((((int64_t)(ok ? id : 0)) * p.H_kv + h) << p.page_shift) + ((key0 + my_row) & inside);
+        };
+        // bf16: k and v of a block into LDS, 1 KiB an instruction
+        auto stage = [&](int key0, int buf, int id) {
+            constexpr int RP = 64 / CH; // rows of an instruction
+            const int64_t cell = first_cell(key0, buf, id);
+            const uint8_t *kp = static_cast<const uint8_t *>(p.k_pages) + cell * ROWB;
+            const uint8_t *vp = static_cast<const uint8_t *>(p.v_pages) + cell * ROWB;
 #pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const int r0 = (wave * PER + q) * RP;
-                const int64_t cell = cell_of(key0 + r0);
-                const int rl = lane / CH;
-                const int off = rl * ROWB + ((lane % CH) ^ swizzle(r0 + rl)) * 16;
-                const uint8_t *kp = static_cast<const uint8_t *>(p.k_pages) + cell * ROWB;
-                const uint8_t *vp = static_cast<const uint8_t *>(p.v_pages) + cell * ROWB;
-                __builtin_amdgcn_global_load_lds((global_u32 *)(kp + off), (lds_u32 *)&sm_k[buf][r0 * ROWB], 16, 0, 0);
-                __builtin_amdgcn_global_load_lds((global_u32 *)(vp + off), (lds_u32 *)&sm_v[buf][r0 * ROWB], 16, 0, 0);
+            for (int q = 0; q < WR / RP; ++q) {
+                const int r0 = my_row + q * RP, rl = lane / CH;
+                const int off = (q * RP + rl) * ROWB + ((lane % CH) ^ swizzle(r0 + rl)) * 16;
+                load_to_lds(&sm_k[buf][r0 * ROWB], kp, off);
+                load_to_lds(&sm_v[buf][r0 * ROWB], vp, off);
             }
         };
-        // e4m3: through registers, 16 values at a time, which become two chunks
-        constexpr int PE = KB * D / 16 > NT ? KB * D / 16 / NT : 1;
-        u32x4 ek[PE], ev[PE];
-        auto fetch = [&](int key0) {
-#pragma unroll
-            for (int q = 0; q < PE; ++q) {
-                const int x = tid + q * NT, r0 = x / (D / 16), c = x % (D / 16);
-                if (r0 < KB) {
-                    const int64_t cell = cell_of(key0 + r0);
-                    ek[q] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.k_pages) + cell * D + c * 16);
-                    ev[q] = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.v_pages) + cell * D + c * 16);
-                }
+        // e4m3: through registers, 16 values a lane, which become two chunks
+        u32x4 ek, ev;
+        const int er = my_row + lane / (D / 16), ec = lane % (D / 16);
+        auto fetch = [&](int key0, int buf, int id) {
+            const int64_t cell = first_cell(key0, buf, id);
+            if (my_row < KB) {
+                const int off = lane * 16;
+                ek = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.k_pages) + cell * D + off);
+                ev = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.v_pages) + cell * D + off);
             }
         };
         auto put = [&](int buf) {
+            if (my_row < KB) {
 #pragma unroll
-            for (int q = 0; q < PE; ++q) {
-                const int x = tid + q * NT, r0 = x / (D / 16), c = x % (D / 16);
-                if (r0 < KB) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int at = r0 * ROWB + ((2 * c + y) ^ swizzle(r0)) * 16;
-                        *reinterpret_cast<u32x4 *>(&sm_k[buf][at]) =
-                            u32x4{e4m3_to_bf16<false>(ek[q][2 * y]), e4m3_to_bf16<true>(ek[q][2 * y]),
-                                  e4m3_to_bf16<false>(ek[q][2 * y + 1]), e4m3_to_bf16<true>(ek[q][2 * y + 1])};
-                        *reinterpret_cast<u32x4 *>(&sm_v[buf][at]) =
-                            u32x4{e4m3_to_bf16<false>(ev[q][2 * y]), e4m3_to_bf16<true>(ev[q][2 * y]),
-                                  e4m3_to_bf16<false>(ev[q][2 * y + 1]), e4m3_to_bf16<true>(ev[q][2 * y + 1])};
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    const int at = er * ROWB + ((2 * ec + y) ^ swizzle(er)) * 16;
+                    *reinterpret_cast<u32x4 *>(&sm_k[buf][at]) =
+                        u32x4{e4m3_to_bf16<false>(ek[2 * y]), e4m3_to_bf16<true>(ek[2 * y]),
+                              e4m3_to_bf16<false>(ek[2 * y + 1]), e4m3_to_bf16<true>(ek[2 * y + 1])};
+                    *reinterpret_cast<u32x4 *>(&sm_v[buf][at]) =
+                        u32x4{e4m3_to_bf16<false>(ev[2 * y]), e4m3_to_bf16<true>(ev[2 * y]),
+                              e4m3_to_bf16<false>(ev[2 * y + 1]), e4m3_to_bf16<true>(ev[2 * y + 1])};
                 }
             }
         };
 
         const int end = span.hi > span.lo ? blk1 : blk0; // no keys: nothing to walk
         __syncthreads(); // the buffers of the piece before are read
-        if (tid < 2)
+        if (tid < 2) {
             sm_odd[tid] = 0;
+            *reinterpret_cast<uint32_t *>(sm_lost[tid]) = 0;
+        }
+        __syncthreads();
+        int id = 0; // of the block after the one that is staged last
         if (blk0 < end) {
-            find_missing(span.lo + blk0 * KB);
+            const int key0 = span.lo + blk0 * KB;
+            id = next_page(key0);
             if constexpr (E4M3) {
-                fetch(span.lo + blk0 * KB);
+                fetch(key0, 0, id);
                 put(0);
             } else {
-                stage(span.lo + blk0 * KB, 0);
+                stage(key0, 0, id);
             }
+            id = next_page(key0 + KB);
         }
         for (int blk = blk0; blk < end; ++blk) {
             const int buf = (blk - blk0) & 1, key0 = span.lo + blk * KB;
-            const int lost = missing;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // this wave's part of the block is in LDS
             __syncthreads();
+            const uint32_t lost = *reinterpret_cast<const uint32_t *>(sm_lost[buf]);
             if (blk + 1 < end) {
-                find_missing(key0 + KB);
                 if constexpr (E4M3)
-                    fetch(key0 + KB);
+                    fetch(key0 + KB, buf ^ 1, id);
                 else
-                    stage(key0 + KB, buf ^ 1);
+                    stage(key0 + KB, buf ^ 1, id);
+                id = next_page(key0 + 2 * KB);
             }
             // A block that some row does not see whole: v of keys past the sequence's last is cleared,
             // and so are infinities and NaN, which 0 times would carry into rows that do not see them.
@@ -409,7 +423,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                     for (int q = 0; q < KB / 16; ++q)
 #pragma unroll
                         for (int x = 0; x < RS; ++x)
-                            bad[x] |= (lost >> q & 1) && pos[x] >= key0 + 16 * q && pos[x] - reach <= key0 + 16 * q + 15;
+                            bad[x] |= (lost >> (8 * q) & 1) && pos[x] >= key0 + 16 * q && pos[x] - reach <= key0 + 16 * q + 15;
                 }
                 // the LDS addresses are formed anew each block: kept, they cost 16 registers
                 int k_at = k_chunk, v_at[2] = {v_base[0], v_base[1]};
@@ -425,23 +439,37 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 sc[x][y][i] = 0.f;
+                    // The LDS reads of the next few products leave before these: left to itself the
+                    // compiler reads, waits and multiplies one by one.
+                    u32x4 kf[2][KA], ql[2][KA];
+                    auto read_k = [&](int g) {
 #pragma unroll
-                    for (int i = 0; i < ST; ++i)
-#pragma unroll
-                        for (int y = 0; y < NS; ++y) {
-                            const u32x4 kf = *reinterpret_cast<const u32x4 *>(
+                        for (int k = 0; k < KA; ++k) {
+                            const int i = (g * KA + k) / NS, y = (g * KA + k) % NS;
+                            kf[g & 1][k] = *reinterpret_cast<const u32x4 *>(
                                 kb + y * 32 * ROWB + k_row + (k_at ^ ((i & 7) * 32)) + (i >> 3) * 256);
-#pragma unroll
-                            for (int x = 0; x < RS; ++x) {
-                                bf16x8 q;
-                                if (i < QL)
-                                    q = __builtin_bit_cast(bf16x8, sm_q[((wave * RS + x) * QL + i) * 64 + lane]);
-                                else
-                                    q = qf[x][i - QL];
-                                sc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf), q,
-                                                                                   sc[x][y], 0, 0, 0);
-                            }
+                            if (i < QL)
+                                ql[g & 1][k] = sm_q[(wave * QL + i) * 64 + lane];
                         }
+                    };
+                    read_k(0);
+#pragma unroll
+                    for (int g = 0; g < ST * NS / KA; ++g) {
+                        if (g + 1 < ST * NS / KA)
+                            read_k(g + 1);
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int k = 0; k < KA; ++k) {
+                            const int i = (g * KA + k) / NS, y = (g * KA + k) % NS;
+#pragma unroll
+                            for (int x = 0; x < RS; ++x)
+                                sc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                    __builtin_bit_cast(bf16x8, kf[g & 1][k]),
+                                    i < QL ? __builtin_bit_cast(bf16x8, ql[g & 1][k]) : qf[x][i < QL ? 0 : i - QL],
+                                    sc[x][y], 0, 0, 0);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
 #pragma unroll
                     for (int x = 0; x < RS; ++x)
 #pragma unroll
@@ -485,32 +513,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                             m[x] = m_new;
                         }
                     }
-                    bf16x8 pf[RS][2 * NS];
+                    // weights of 16 keys at a time, and the products with their v
+                    constexpr int VA = D == 256 ? 2 : (DT < 4 ? DT : 4), VG = DT / VA; // products at a time
+                    u32x4 vf[2][VA];
+                    auto read_v = [&](int g) {
 #pragma unroll
-                    for (int x = 0; x < RS; ++x) {
-                        const float off = m[x] == neg_inf() ? 0.f : -m[x];
-                        float sum = 0.f;
-#pragma unroll
-                        for (int q = 0; q < 2 * NS; ++q) {
-                            float e[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                e[i] = __builtin_amdgcn_exp2f(fmaf(sc[x][q >> 1][8 * (q & 1) + i], scale, off));
-                                sum += e[i];
-                            }
-                            // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and
-                            // o is rounded to bf16 in the end
-                            pf[x][q] = __builtin_bit_cast(bf16x8,
-                                                          u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
-                                                                pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
-                        }
-                        l[x] += sum;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2 * NS; ++q)
-#pragma unroll
-                        for (int a = 0; a < DT; ++a) {
-                            u32x4 vf;
+                        for (int k = 0; k < VA; ++k) {
+                            const int q = g / VG, a = (g % VG) * VA + k;
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const u32x2 v2 = __builtin_bit_cast(
@@ -518,14 +527,48 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                                                (__attribute__((address_space(3))) s16x4 *)(vb + q * 16 * ROWB +
                                                                                            (v_at[y] ^ ((a & 3) * 64)) +
                                                                                            (a >> 2) * 256)));
-                                vf[2 * y] = v2[0];
-                                vf[2 * y + 1] = v2[1];
+                                vf[g & 1][k][2 * y] = v2[0];
+                                vf[g & 1][k][2 * y + 1] = v2[1];
                             }
-#pragma unroll
-                            for (int x = 0; x < RS; ++x)
-                                acc[x][a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf),
-                                                                                    pf[x][q], acc[x][a], 0, 0, 0);
                         }
+                    };
+                    bf16x8 pf[2][RS];
+                    auto weigh = [&](int q) {
+#pragma unroll
+                        for (int x = 0; x < RS; ++x) {
+                            const float off = m[x] == neg_inf() ? 0.f : -m[x];
+                            float e[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                e[i] = __builtin_amdgcn_exp2f(fmaf(sc[x][q >> 1][8 * (q & 1) + i], scale, off));
+                                l[x] += e[i];
+                            }
+                            // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and
+                            // o is rounded to bf16 in the end
+                            pf[q & 1][x] = __builtin_bit_cast(bf16x8,
+                                                              u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                                                    pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
+                        }
+                    };
+                    read_v(0);
+                    weigh(0);
+#pragma unroll
+                    for (int g = 0; g < 2 * NS * VG; ++g) {
+                        const int q = g / VG;
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (g + 1 < 2 * NS * VG)
+                            read_v(g + 1);
+                        if (g % VG == VG - 1 && q + 1 < 2 * NS)
+                            weigh(q + 1);
+#pragma unroll
+                        for (int k = 0; k < VA; ++k)
+#pragma unroll
+                            for (int x = 0; x < RS; ++x) {
+                                f32x16 &o = acc[x][(g % VG) * VA + k];
+                                o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]),
+                                                                            pf[q & 1][x], o, 0, 0, 0);
+                            }
+                    }
                     if (odd) { // uniform: what left the product goes to the rows that see it
                         for (int j = 0; j < KB && key0 + j < s.L; ++j) {
                             const int64_t cell = cell_of(key0 + j) * D;
