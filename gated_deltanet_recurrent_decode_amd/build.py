@@ -38,6 +38,9 @@ FLAGS = [
 PER_SOURCE = {
     "gdn_step_tile.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=8"],
     "gdn_step.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=3"],
+    # its inner loop needs nearly all of the 256 registers two waves a SIMD have: addresses
+    # formed ahead of the loop spill
+    "attn_tiles.hip": ["-mllvm", "-disable-machine-licm", "-mllvm", "-amdgpu-use-amdgpu-trackers=1"],
     # the calibration copies, so that their slot loads leave as early as the step's
     "traffic_probe.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=9"],
 }

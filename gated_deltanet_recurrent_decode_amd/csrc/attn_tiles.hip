@@ -30,7 +30,7 @@ namespace {
 
 constexpr int TR = 256;  // rows of a tile
 // keys of a block: with 256 columns the queries take half of the LDS
-constexpr int block_keys(int d) { return d == 256 ? 32 : 64; }
+constexpr int block_keys(int d) { return d == 256 ? 32 : 128; }
 constexpr int PT = 1024; // the planning workgroup
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -191,14 +191,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     constexpr int DT = D / 32;                // 32-column tiles of o
     constexpr int ROWB = D * 2;               // bytes of an LDS row
     constexpr int KB = block_keys(D);
-    constexpr int NS = KB / 32;
-    constexpr int KA = D == 256 ? (E4M3 ? 1 : 2) : 4; // products whose LDS reads go ahead together
+    constexpr int SB = D == 256 ? 32 : 64;    // keys of a softmax step
+    constexpr int NS = SB / 32;
+    constexpr int KA = D == 256 ? 1 : 4; // products whose LDS reads go ahead together
     // steps whose queries a lane keeps in LDS, each lane its own: all 16 of 256 columns in
     // registers, beside 128 of o, spill
     constexpr int QL = D == 256 ? 11 : 0;
     __shared__ __align__(16) uint8_t sm_k[2][KB * ROWB], sm_v[2][KB * ROWB];
     __shared__ int sm_odd[2];
-    __shared__ __align__(4) uint8_t sm_lost[2][4]; // a block's 16-key parts whose page is outside the pool
+    __shared__ __align__(8) uint8_t sm_lost[2][8]; // a block's 16-key parts whose page is outside the pool
     __shared__ u32x4 sm_q[QL ? NW * RS * QL * 64 : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -305,99 +306,149 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
         };
         // Staging: a wave brings the same few rows of every block, all of them on one page.  Its
         // number is read a block ahead, by the scalar unit.
-        constexpr int WR = E4M3 ? 1024 / D : KB / NW; // rows of a wave
+        constexpr int WR = KB / NW; // rows of a wave
+        static_assert(WR <= 16, "on one page");
         const int my_row = wave * WR;
         auto *table = (__attribute__((address_space(4))) const int32_t *)tab;
         auto next_page = [&](int key0) {
             const int key = uniform(key0 + my_row);
-            return my_row < KB && key < s.L ? table[key >> p.page_shift] : 0;
+            return key < s.L ? table[key >> p.page_shift] : 0;
         };
-        auto first_cell = [&](int key0, int buf, int id) { // of the wave's rows
-            const bool ok = id > 0 && id < p.N;
-            if (lane == 0 && my_row < KB)
-                sm_lost[buf][my_row >> 4] = !ok && key0 + my_row < s.L;
-            return ((((int64_t)(ok ? id : 0)) * p.H_kv + h) << p.page_shift) + ((key0 + my_row) & inside);
+        auto first_cell = [&](int key0, int id) { // of the wave's rows
+            return ((((int64_t)(id > 0 && id < p.N ? id : 0)) * p.H_kv + h) << p.page_shift) +
+                   ((key0 + my_row) & inside);
         };
-        // bf16: k and v of a block into LDS, 1 KiB an instruction
-        auto stage = [&](int key0, int buf, int id) {
+        // bf16: k or v of a block into LDS, 1 KiB an instruction
+        auto stage = [&](const void *pages, uint8_t *to, int key0, int id) {
             constexpr int RP = 64 / CH; // rows of an instruction
-            const int64_t cell = first_cell(key0, buf, id);
-            const uint8_t *kp = static_cast<const uint8_t *>(p.k_pages) + cell * ROWB;
-            const uint8_t *vp = static_cast<const uint8_t *>(p.v_pages) + cell * ROWB;
+            const uint8_t *from = static_cast<const uint8_t *>(pages) + first_cell(key0, id) * ROWB;
 #pragma unroll
             for (int q = 0; q < WR / RP; ++q) {
                 const int r0 = my_row + q * RP, rl = lane / CH;
-                const int off = (q * RP + rl) * ROWB + ((lane % CH) ^ swizzle(r0 + rl)) * 16;
-                load_to_lds(&sm_k[buf][r0 * ROWB], kp, off);
-                load_to_lds(&sm_v[buf][r0 * ROWB], vp, off);
+                load_to_lds(to + r0 * ROWB, from, (q * RP + rl) * ROWB + ((lane % CH) ^ swizzle(r0 + rl)) * 16);
             }
         };
         // e4m3: through registers, 16 values a lane, which become two chunks
-        u32x4 ek, ev;
+        constexpr int ER = 1024 / D, PE = WR / ER > 0 ? WR / ER : 1; // rows of a load, loads
+        u32x4 ek[PE], ev[PE];
         const int er = my_row + lane / (D / 16), ec = lane % (D / 16);
-        auto fetch = [&](int key0, int buf, int id) {
-            const int64_t cell = first_cell(key0, buf, id);
-            if (my_row < KB) {
-                const int off = lane * 16;
-                ek = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.k_pages) + cell * D + off);
-                ev = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(p.v_pages) + cell * D + off);
-            }
+        auto fetch = [&](const void *pages, u32x4(&x)[PE], int key0, int id) {
+            const uint8_t *from = static_cast<const uint8_t *>(pages) + first_cell(key0, id) * D + lane * 16;
+#pragma unroll
+            for (int q = 0; q < PE; ++q)
+                x[q] = *reinterpret_cast<const u32x4 *>(from + q * 1024);
         };
-        auto put = [&](int buf) {
-            if (my_row < KB) {
+        auto put = [&](uint8_t *to, const u32x4(&x)[PE]) {
+#pragma unroll
+            for (int q = 0; q < PE; ++q)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int at = er * ROWB + ((2 * ec + y) ^ swizzle(er)) * 16;
-                    *reinterpret_cast<u32x4 *>(&sm_k[buf][at]) =
-                        u32x4{e4m3_to_bf16<false>(ek[2 * y]), e4m3_to_bf16<true>(ek[2 * y]),
-                              e4m3_to_bf16<false>(ek[2 * y + 1]), e4m3_to_bf16<true>(ek[2 * y + 1])};
-                    *reinterpret_cast<u32x4 *>(&sm_v[buf][at]) =
-                        u32x4{e4m3_to_bf16<false>(ev[2 * y]), e4m3_to_bf16<true>(ev[2 * y]),
-                              e4m3_to_bf16<false>(ev[2 * y + 1]), e4m3_to_bf16<true>(ev[2 * y + 1])};
+                    const int r = er + q * ER;
+                    *reinterpret_cast<u32x4 *>(to + r * ROWB + ((2 * ec + y) ^ swizzle(r)) * 16) =
+                        u32x4{e4m3_to_bf16<false>(x[q][2 * y]), e4m3_to_bf16<true>(x[q][2 * y]),
+                              e4m3_to_bf16<false>(x[q][2 * y + 1]), e4m3_to_bf16<true>(x[q][2 * y + 1])};
                 }
-            }
         };
 
         const int end = span.hi > span.lo ? blk1 : blk0; // no keys: nothing to walk
+        auto note = [&](int key0, int slot, int id) { // whether the wave's keys have a usable page
+            if (lane == 0)
+                sm_lost[slot][my_row >> 4] = !(id > 0 && id < p.N) && key0 + my_row < s.L;
+        };
         __syncthreads(); // the buffers of the piece before are read
         if (tid < 2) {
             sm_odd[tid] = 0;
-            *reinterpret_cast<uint32_t *>(sm_lost[tid]) = 0;
+            *reinterpret_cast<uint64_t *>(sm_lost[tid]) = 0;
         }
         __syncthreads();
-        int id = 0; // of the block after the one that is staged last
-        if (blk0 < end) {
-            const int key0 = span.lo + blk0 * KB;
-            id = next_page(key0);
-            if constexpr (E4M3) {
-                fetch(key0, 0, id);
-                put(0);
-            } else {
-                stage(key0, 0, id);
-            }
+        const int first_key = span.lo + blk0 * KB;
+        int id = 0; // page of the block that is staged next
+        auto bring = [&](int key0, int buf) {
+            note(key0, buf, id);
+            stage(p.k_pages, sm_k[buf], key0, id);
+            stage(p.v_pages, sm_v[buf], key0, id);
             id = next_page(key0 + KB);
+        };
+        auto bring_e4m3 = [&](int key0, int buf) {
+            note(key0, buf, id);
+            fetch(p.k_pages, ek, key0, id);
+            fetch(p.v_pages, ev, key0, id);
+            id = next_page(key0 + KB);
+        };
+        if (blk0 < end) {
+            id = next_page(first_key);
+            if constexpr (E4M3) {
+                bring_e4m3(first_key, 0);
+                put(sm_k[0], ek);
+                put(sm_v[0], ev);
+            } else {
+                bring(first_key, 0);
+            }
         }
+        auto read_k = [&](const uint8_t *kb, int at, int j) { // k of product j: step j / NS, part j % NS
+            return *reinterpret_cast<const u32x4 *>(kb + (j % NS) * 32 * ROWB + k_row + (at ^ ((j / NS & 7) * 32)) +
+                                                    (j / NS >> 3) * 256);
+        };
+        auto step_q = [&](int x, int i) {
+            return i < QL ? __builtin_bit_cast(bf16x8, sm_q[(wave * QL + i) * 64 + lane]) : qf[x][i < QL ? 0 : i - QL];
+        };
+        // all scores of a block
+        auto score = [&](const uint8_t *kb, f32x16(&sc)[RS][NS]) {
+            // the LDS addresses are formed anew each block: kept, they cost 8 registers
+            int k_at = k_chunk;
+            asm volatile("" : "+v"(k_at));
+#pragma unroll
+            for (int x = 0; x < RS; ++x)
+#pragma unroll
+                for (int y = 0; y < NS; ++y)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sc[x][y][i] = 0.f;
+            // The LDS reads of the next few products leave before these: left to itself the
+            // compiler reads, waits and multiplies one by one.
+            u32x4 kf[2][KA];
+            bf16x8 ql[2][KA];
+#pragma unroll
+            for (int g = -1; g < ST * NS / KA; ++g) {
+                if (g + 1 < ST * NS / KA)
+#pragma unroll
+                    for (int k = 0; k < KA; ++k) {
+                        kf[(g + 1) & 1][k] = read_k(kb, k_at, (g + 1) * KA + k);
+                        ql[(g + 1) & 1][k] = step_q(0, ((g + 1) * KA + k) / NS);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+                if (g >= 0)
+#pragma unroll
+                    for (int k = 0; k < KA; ++k) {
+                        f32x16 &o = sc[0][(g * KA + k) % NS];
+                        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g & 1][k]),
+                                                                    ql[g & 1][k], o, 0, 0, 0);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto sees = [&](int key0) { // some row of the wave sees some key of the block
+            return any && key0 <= max_pos && !(p.window > 0 && key0 + SB - 1 <= min_pos - p.window);
+        };
         for (int blk = blk0; blk < end; ++blk) {
-            const int buf = (blk - blk0) & 1, key0 = span.lo + blk * KB;
+            const int buf = (blk - blk0) & 1, block0 = span.lo + blk * KB;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // this wave's part of the block is in LDS
             __syncthreads();
-            const uint32_t lost = *reinterpret_cast<const uint32_t *>(sm_lost[buf]);
             if (blk + 1 < end) {
                 if constexpr (E4M3)
-                    fetch(key0 + KB, buf ^ 1, id);
+                    bring_e4m3(block0 + KB, buf ^ 1);
                 else
-                    stage(key0 + KB, buf ^ 1, id);
-                id = next_page(key0 + 2 * KB);
+                    bring(block0 + KB, buf ^ 1);
             }
             // A block that some row does not see whole: v of keys past the sequence's last is cleared,
             // and so are infinities and NaN, which 0 times would carry into rows that do not see them.
             bool odd = false;
-            if (key0 + KB - 1 > span.min_pos || (p.window > 0 && key0 <= span.max_pos - p.window)) {
+            if (block0 + KB - 1 > span.min_pos || (p.window > 0 && block0 <= span.max_pos - p.window)) {
                 if (tid == 0)
                     sm_odd[buf ^ 1] = 0;
 #pragma unroll
                 for (int q = 0; q < KB * CH / NT; ++q) {
-                    const int x = tid + q * NT, key = key0 + x / CH;
+                    const int x = tid + q * NT, key = block0 + x / CH;
                     u32x4 *at = reinterpret_cast<u32x4 *>(&sm_v[buf][x * 16]);
                     u32x4 v = *at;
                     bool found = false;
@@ -417,59 +468,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                 __syncthreads();
                 odd = sm_odd[buf] != 0;
             }
-            if (any && key0 <= max_pos && !(p.window > 0 && key0 + KB - 1 <= min_pos - p.window)) {
+            // scores, weights and products of SB keys at a time: registers allow no more
+#pragma unroll 1
+            for (int sub = 0; sub < KB / SB; ++sub) {
+            const int key0 = block0 + sub * SB;
+            if (sees(key0)) {
+                const uint64_t lost = *reinterpret_cast<const uint64_t *>(sm_lost[buf]) >> (sub * (SB / 2));
                 if (lost) {
 #pragma unroll
-                    for (int q = 0; q < KB / 16; ++q)
+                    for (int q = 0; q < SB / 16; ++q)
 #pragma unroll
                         for (int x = 0; x < RS; ++x)
                             bad[x] |= (lost >> (8 * q) & 1) && pos[x] >= key0 + 16 * q && pos[x] - reach <= key0 + 16 * q + 15;
                 }
-                // the LDS addresses are formed anew each block: kept, they cost 16 registers
-                int k_at = k_chunk, v_at[2] = {v_base[0], v_base[1]};
-                asm volatile("" : "+v"(k_at), "+v"(v_at[0]), "+v"(v_at[1]));
-                const bool mixed = key0 + KB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
-                const uint8_t *kb = sm_k[buf], *vb = sm_v[buf];
+                int v_at[2] = {v_base[0], v_base[1]};
+                asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
+                const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
+                const uint8_t *vb = sm_v[buf] + sub * SB * ROWB;
                 {
                     f32x16 sc[RS][NS];
-#pragma unroll
-                    for (int x = 0; x < RS; ++x)
-#pragma unroll
-                        for (int y = 0; y < NS; ++y)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sc[x][y][i] = 0.f;
-                    // The LDS reads of the next few products leave before these: left to itself the
-                    // compiler reads, waits and multiplies one by one.
-                    u32x4 kf[2][KA], ql[2][KA];
-                    auto read_k = [&](int g) {
-#pragma unroll
-                        for (int k = 0; k < KA; ++k) {
-                            const int i = (g * KA + k) / NS, y = (g * KA + k) % NS;
-                            kf[g & 1][k] = *reinterpret_cast<const u32x4 *>(
-                                kb + y * 32 * ROWB + k_row + (k_at ^ ((i & 7) * 32)) + (i >> 3) * 256);
-                            if (i < QL)
-                                ql[g & 1][k] = sm_q[(wave * QL + i) * 64 + lane];
-                        }
-                    };
-                    read_k(0);
-#pragma unroll
-                    for (int g = 0; g < ST * NS / KA; ++g) {
-                        if (g + 1 < ST * NS / KA)
-                            read_k(g + 1);
-                        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                        for (int k = 0; k < KA; ++k) {
-                            const int i = (g * KA + k) / NS, y = (g * KA + k) % NS;
-#pragma unroll
-                            for (int x = 0; x < RS; ++x)
-                                sc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                    __builtin_bit_cast(bf16x8, kf[g & 1][k]),
-                                    i < QL ? __builtin_bit_cast(bf16x8, ql[g & 1][k]) : qf[x][i < QL ? 0 : i - QL],
-                                    sc[x][y], 0, 0, 0);
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    score(sm_k[buf] + sub * SB * ROWB, sc);
 #pragma unroll
                     for (int x = 0; x < RS; ++x)
 #pragma unroll
@@ -513,10 +531,37 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                             m[x] = m_new;
                         }
                     }
-                    // weights of 16 keys at a time, and the products with their v
+                    if (odd) { // uniform: what left v goes to the rows that see it
+#pragma unroll 1
+                        for (int j = 0; j < SB && key0 + j < s.L; ++j) {
+                            const uint8_t *v = static_cast<const uint8_t *>(p.v_pages) +
+                                               cell_of(key0 + j) * (E4M3 ? D : ROWB) + hh * (E4M3 ? 4 : 8);
+                            const int back = pos[0] - (key0 + j);
+                            const bool seen = back >= 0 && back <= reach;
+#pragma unroll
+                            for (int c = 0; c < DT * 4; ++c) { // four columns of this lane's
+                                u32x2 y;
+                                if constexpr (E4M3) {
+                                    const uint32_t z = *reinterpret_cast<const uint32_t *>(v + c * 8);
+                                    y = u32x2{e4m3_to_bf16<false>(z), e4m3_to_bf16<true>(z)};
+                                } else {
+                                    y = *reinterpret_cast<const u32x2 *>(v + c * 16);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t z = (i & 1) ? y[i >> 1] & 0xffff0000u : y[i >> 1] << 16;
+                                    if (seen && (z & 0x7f800000u) == 0x7f800000u)
+                                        acc[0][c >> 2][(c & 3) * 4 + i] += __uint_as_float(z);
+                                }
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                        }
+                    }
+                    // weights of 16 keys at a time, and the products with their v beside the next ones
                     constexpr int VA = D == 256 ? 2 : (DT < 4 ? DT : 4), VG = DT / VA; // products at a time
+                    constexpr int GROUPS = 2 * NS * VG;
                     u32x4 vf[2][VA];
-                    auto read_v = [&](int g) {
+                    auto read_ahead = [&](int g) {
 #pragma unroll
                         for (int k = 0; k < VA; ++k) {
                             const int q = g / VG, a = (g % VG) * VA + k;
@@ -532,70 +577,47 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                             }
                         }
                     };
-                    bf16x8 pf[2][RS];
-                    auto weigh = [&](int q) {
+                    uint32_t pw[2][4]; // two groups of weights, bf16 pairs
+                    const float off = m[0] == neg_inf() ? 0.f : -m[0];
+                    auto weigh = [&](int q, int i0, int i1) { // values i0 .. i1 - 1 of 16 keys' eight
 #pragma unroll
-                        for (int x = 0; x < RS; ++x) {
-                            const float off = m[x] == neg_inf() ? 0.f : -m[x];
-                            float e[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                e[i] = __builtin_amdgcn_exp2f(fmaf(sc[x][q >> 1][8 * (q & 1) + i], scale, off));
-                                l[x] += e[i];
-                            }
+                        for (int i = i0; i < i1; i += 2) {
+                            const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[0][q >> 1][8 * (q & 1) + i], scale, off));
+                            const float e1 =
+                                __builtin_amdgcn_exp2f(fmaf(sc[0][q >> 1][8 * (q & 1) + i + 1], scale, off));
+                            l[0] += e0 + e1;
                             // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and
                             // o is rounded to bf16 in the end
-                            pf[q & 1][x] = __builtin_bit_cast(bf16x8,
-                                                              u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
-                                                                    pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
+                            pw[q & 1][i >> 1] = pack_bf16(e0, e1);
                         }
                     };
-                    read_v(0);
-                    weigh(0);
+                    read_ahead(0);
+                    weigh(0, 0, 8);
 #pragma unroll
-                    for (int g = 0; g < 2 * NS * VG; ++g) {
-                        const int q = g / VG;
+                    for (int g = 0; g < GROUPS; ++g) {
+                        const int q = g / VG, part = g % VG;
                         __builtin_amdgcn_sched_barrier(0);
-                        if (g + 1 < 2 * NS * VG)
-                            read_v(g + 1);
-                        if (g % VG == VG - 1 && q + 1 < 2 * NS)
-                            weigh(q + 1);
+                        if (g + 1 < GROUPS)
+                            read_ahead(g + 1);
+                        if (q + 1 < 2 * NS)
+                            weigh(q + 1, part * 8 / VG, (part + 1) * 8 / VG);
+                        const bf16x8 pf = __builtin_bit_cast(
+                            bf16x8, u32x4{pw[q & 1][0], pw[q & 1][1], pw[q & 1][2], pw[q & 1][3]});
 #pragma unroll
-                        for (int k = 0; k < VA; ++k)
-#pragma unroll
-                            for (int x = 0; x < RS; ++x) {
-                                f32x16 &o = acc[x][(g % VG) * VA + k];
-                                o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]),
-                                                                            pf[q & 1][x], o, 0, 0, 0);
-                            }
-                    }
-                    if (odd) { // uniform: what left the product goes to the rows that see it
-                        for (int j = 0; j < KB && key0 + j < s.L; ++j) {
-                            const int64_t cell = cell_of(key0 + j) * D;
-#pragma unroll
-                            for (int a = 0; a < DT; ++a)
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const int64_t at = cell + a * 32 + 8 * (i >> 2) + 4 * hh + (i & 3);
-                                    uint32_t y;
-                                    if constexpr (E4M3)
-                                        y = e4m3_to_bf16<false>(static_cast<const uint8_t *>(p.v_pages)[at]) << 16;
-                                    else
-                                        y = (uint32_t) static_cast<const uint16_t *>(p.v_pages)[at] << 16;
-#pragma unroll
-                                    for (int x = 0; x < RS; ++x) {
-                                        const int back = pos[x] - (key0 + j);
-                                        if (back >= 0 && back <= reach && (y & 0x7f800000u) == 0x7f800000u)
-                                            acc[x][a][i] += __uint_as_float(y);
-                                    }
-                                }
+                        for (int k = 0; k < VA; ++k) {
+                            f32x16 &o = acc[0][part * VA + k];
+                            o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]), pf, o,
+                                                                        0, 0, 0);
                         }
                     }
                 }
             }
+            }
             if constexpr (E4M3) {
-                if (blk + 1 < end)
-                    put(buf ^ 1);
+                if (blk + 1 < end) {
+                    put(sm_k[buf ^ 1], ek);
+                    put(sm_v[buf ^ 1], ev);
+                }
             }
         }
 #pragma unroll
