@@ -125,12 +125,14 @@ def _at_or_none(t, name, dtype, device):
     return 0 if t is None else _at(t, name, dtype, device)
 
 
-def _strided(t, name, dtype, device):
-    """Packed heads as the C structure: address, row and head strides."""
+def _heads(t, name, T, H, d, dtype, device):
+    """Packed heads [T][H][d] as the C structure: address, row and head strides."""
+    s, step = t.shape, t.stride()
+    if s != (T, H, d) or step[2] != 1:
+        _heads_layout(t, name, T, H, d)
     if t.dtype is not dtype or t.get_device() != device:
         _refuse(t, name, dtype, device)
-    s = t.stride()
-    return _HEADS.pack(t.data_ptr(), s[0], s[1])
+    return _HEADS.pack(t.data_ptr(), step[0], step[1])
 
 
 def _launch(name, call, device, stream, *args):
@@ -200,14 +202,21 @@ def _packed_layout(row, cu_seqlens):
     return a[0]
 
 
-def _heads_layout(t, name, T, H, d):
-    """[T][H][d] with contiguous d; returns H."""
+def _packed_heads(t, name):
+    """Tokens and heads of a tensor [T][H][d]."""
     s = t.shape
-    if len(s) != 3 or s[0] != T or s[2] != d or (H is not None and s[1] != H):
-        raise ValueError(f"{name} must be [{T}][{'H' if H is None else H}][{d}], got {list(s)}")
+    if len(s) != 3:
+        raise ValueError(f"{name} must be [T][H][d], got {list(s)}")
+    return s[0], s[1]
+
+
+def _heads_layout(t, name, T, H, d):
+    """Refuses anything but [T][H][d] with contiguous d."""
+    s = t.shape
+    if len(s) != 3 or s[0] != T or s[2] != d or s[1] != H:
+        raise ValueError(f"{name} must be [{T}][{H}][{d}], got {list(s)}")
     if t.stride(2) != 1:
         raise ValueError(f"{name}: the head's values must be contiguous")
-    return s[1]
 
 
 # ------------------------------------------------------------------ entry points
@@ -234,7 +243,7 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
     like q (or q itself); freqs [rot/2] float64 or None; row [B], cu_seqlens [B+1] int32.  q and q_out may be
     None, and so may k and v (page_table may then be None too)."""
     torch = _torch()
-    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    bf, i32 = torch.bfloat16, torch.int32
     if q is None and k is None:
         raise ValueError("nothing to do: q or k and v are required")
     if (q is None) != (q_out is None) or (k is None) != (v is None):
@@ -245,17 +254,14 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
     hq = ho = hk = hv = rope = norm = None
     H_q = H_kv
     if q is not None:
-        T = q.shape[0]
-        H_q = _heads_layout(q, "q", T, None, d)
-        _heads_layout(q_out, "q_out", T, H_q, d)
-        hq, ho = _strided(q, "q", bf, dev), _strided(q_out, "q_out", bf, dev)
+        T, H_q = _packed_heads(q, "q")
+        hq, ho = _heads(q, "q", T, H_q, d, bf, dev), _heads(q_out, "q_out", T, H_q, d, bf, dev)
     if k is not None:
-        T = k.shape[0] if q is None else T
+        if q is None:
+            T, _ = _packed_heads(k, "k")
         if page_table is None:
             raise ValueError("page_table is required to store k and v")
-        _heads_layout(k, "k", T, H_kv, d)
-        _heads_layout(v, "v", T, H_kv, d)
-        hk, hv = _strided(k, "k", bf, dev), _strided(v, "v", bf, dev)
+        hk, hv = _heads(k, "k", T, H_kv, d, bf, dev), _heads(v, "v", T, H_kv, d, bf, dev)
     if freqs is not None:
         if freqs.dim() != 1 or 2 * freqs.shape[0] > d:
             raise ValueError("freqs must be [rot/2] with rot <= d")
@@ -295,18 +301,16 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
     bf, i32 = torch.bfloat16, torch.int32
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
     B = _packed_layout(row, cu_seqlens)
-    T = q.shape[0]
-    H_q = _heads_layout(q, "q", T, None, d)
-    _heads_layout(out, "out", T, H_q, d)
+    T, H_q = _packed_heads(q, "q")
     if page_table is None:
         raise ValueError("page_table is required")
     if lse is not None and lse.shape != (T, H_q):
         raise ValueError("lse must be [T][H_q]")
     dev = _gpu(q, "q", bf)
     _launch("attn_paged", lib().attn_paged, dev, stream,
-            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind), _strided(q, "q", bf, dev),
+            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind), _heads(q, "q", T, H_q, d, bf, dev),
             _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev), _at(row, "row", i32, dev),
-            _at(cu_seqlens, "cu_seqlens", i32, dev), _strided(out, "out", bf, dev),
+            _at(cu_seqlens, "cu_seqlens", i32, dev), _heads(out, "out", T, H_q, d, bf, dev),
             _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
             _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
 

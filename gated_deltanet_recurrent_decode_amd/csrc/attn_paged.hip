@@ -550,6 +550,8 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
 
 size_t attn_rows_layout(int d, void *base, AttnParams *p)
 {
+    // two a CU: 8 sequences of 40-131 thousand e4m3 tokens at 32/4 heads of 128 take 117 us, with
+    // one 156, with three 145; 32 sequences of 4 tokens over 0.05-3 thousand 30, 39 and 39
     const int workgroups = 2 * device_cus();
     const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4),
                  cut = round256((size_t)workgroups * 8 * 4);

@@ -31,10 +31,13 @@ namespace {
 constexpr int TR = 256;  // rows of a tile
 // keys of a block: with 256 columns the queries take half of the LDS
 constexpr int block_keys(int d) { return d == 256 ? 32 : 128; }
+constexpr int NW = TR / 32; // waves
+constexpr int NT = 64 * NW;
 constexpr int PT = 1024; // the planning workgroup
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // What a tile of a sequence sees: keys lo .. hi - 1, in blocks from lo on.
 struct Span {
@@ -71,7 +74,7 @@ __device__ __forceinline__ void load_to_lds(uint8_t *to, const uint8_t *base, in
     const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)at)), "v"(off),
                  "s"(base)
-                 : "memory", "m0");
+                 : "memory"); // m0 is reserved: whatever of the compiler's own needs it sets it first
 }
 
 // The entry that holds unit u (before[e] <= u < before[e + 1]): 64 probes a round.
@@ -180,12 +183,9 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
     }
 }
 
-// NW waves of RS times 32 rows.
-template <int D, bool E4M3, int NW, int RS>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams p)
+template <int D, bool E4M3>
+__global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 {
-    static_assert(NW * RS * 32 == TR && RS == 1, "a workgroup's rows");
-    constexpr int NT = 64 * NW;
     constexpr int CH = D / 8;                 // chunks of a row
     constexpr int ST = D / 16;                // steps of a score's contraction
     constexpr int DT = D / 32;                // 32-column tiles of o
@@ -193,14 +193,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
     constexpr int KB = block_keys(D);
     constexpr int SB = D == 256 ? 32 : 64;    // keys of a softmax step
     constexpr int NS = SB / 32;
-    constexpr int KA = D == 256 ? 1 : 4; // products whose LDS reads go ahead together
+    constexpr int KA = D == 256 ? 2 : 4; // products whose LDS reads go ahead together
     // steps whose queries a lane keeps in LDS, each lane its own: all 16 of 256 columns in
     // registers, beside 128 of o, spill
-    constexpr int QL = D == 256 ? 11 : 0;
+    constexpr int QL = D == 256 ? (E4M3 ? 11 : 8) : 0;
     __shared__ __align__(16) uint8_t sm_k[2][KB * ROWB], sm_v[2][KB * ROWB];
     __shared__ int sm_odd[2];
     __shared__ __align__(8) uint8_t sm_lost[2][8]; // a block's 16-key parts whose page is outside the pool
-    __shared__ u32x4 sm_q[QL ? NW * RS * QL * 64 : 1];
+    __shared__ u32x4 sm_q[QL ? NW * QL * 64 : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
@@ -249,16 +249,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
         ++e;
 
         const int rows = s.n * p.G;
-        const int row0 = tile * TR + wave * (32 * RS); // this wave's first
+        const int row0 = tile * TR + wave * 32; // this wave's first
         const bool any = row0 < rows && s.kind == kNormal;
-        int pos[RS]; // of this lane's rows
-#pragma unroll
-        for (int x = 0; x < RS; ++x) {
-            const int row = row0 + 32 * x + n_;
-            pos[x] = row < rows && s.kind == kNormal ? s.L - s.n + row / p.G : -1;
-        }
+        const int row = row0 + n_; // this lane's
+        const int pos = row < rows && s.kind == kNormal ? s.L - s.n + row / p.G : -1;
         const int reach = p.window > 0 ? p.window - 1 : 0x3fffffff; // a row sees keys pos - reach .. pos
-        const int row1 = (rows < row0 + 32 * RS ? rows : row0 + 32 * RS) - 1;
+        const int row1 = (rows < row0 + 32 ? rows : row0 + 32) - 1;
         const int min_pos = uniform(s.L - s.n + row0 / p.G), max_pos = uniform(any ? s.L - s.n + row1 / p.G : -1);
 
         // scores are masked before they are scaled, so the scale has to be positive: a negative
@@ -266,33 +262,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
         float scale = E4M3 ? p.scale * p.k_scale[h] : p.scale;
         const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, wipe = scale == 0.f ? 0u : 0xffffffffu;
         scale = scale == 0.f ? 1.0f : fabsf(scale);
-        bf16x8 qf[RS][ST - QL];
-        float m[RS], l[RS];
-        f32x16 acc[RS][DT];
-        bool bad[RS];
+        bf16x8 qf[ST - QL];
+        float m = neg_inf(), l = 0.f;
+        f32x16 acc[DT];
+        bool bad = false;
+        const int r = row < rows ? row : rows - 1; // rows past the last do as it does, unseen
+        const uint16_t *qp = p.q.p + (int64_t)(s.first + r / p.G) * p.q.row +
+                             (int64_t)(h * p.G + r % p.G) * p.q.head + hh * 8;
 #pragma unroll
-        for (int x = 0; x < RS; ++x) {
-            int r = row0 + 32 * x + n_;
-            r = r < rows ? r : rows - 1; // rows past the last do as it does, unseen
-            const uint16_t *qp = p.q.p + (int64_t)(s.first + r / p.G) * p.q.row +
-                                 (int64_t)(h * p.G + r % p.G) * p.q.head + hh * 8;
-#pragma unroll
-            for (int i = 0; i < ST; ++i) {
-                const u32x4 q = (*reinterpret_cast<const u32x4 *>(qp + i * 16) ^ flip) & wipe;
-                if (i < QL)
-                    sm_q[((wave * RS + x) * QL + i) * 64 + lane] = q;
-                else
-                    qf[x][i - QL] = __builtin_bit_cast(bf16x8, q);
-            }
-            m[x] = neg_inf();
-            l[x] = 0.f;
-            bad[x] = false;
-#pragma unroll
-            for (int a = 0; a < DT; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    acc[x][a][i] = 0.f;
+        for (int i = 0; i < ST; ++i) {
+            const u32x4 q = (*reinterpret_cast<const u32x4 *>(qp + i * 16) ^ flip) & wipe;
+            if (i < QL)
+                sm_q[(wave * QL + i) * 64 + lane] = q;
+            else
+                qf[i - QL] = __builtin_bit_cast(bf16x8, q);
         }
+#pragma unroll
+        for (int a = 0; a < DT; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[a][i] = 0.f;
         const int32_t *tab = p.page_table + (int64_t)s.r * p.width;
         const int inside = (1 << p.page_shift) - 1;
 
@@ -389,21 +378,19 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
             return *reinterpret_cast<const u32x4 *>(kb + (j % NS) * 32 * ROWB + k_row + (at ^ ((j / NS & 7) * 32)) +
                                                     (j / NS >> 3) * 256);
         };
-        auto step_q = [&](int x, int i) {
-            return i < QL ? __builtin_bit_cast(bf16x8, sm_q[(wave * QL + i) * 64 + lane]) : qf[x][i < QL ? 0 : i - QL];
+        auto step_q = [&](int i) {
+            return i < QL ? __builtin_bit_cast(bf16x8, sm_q[(wave * QL + i) * 64 + lane]) : qf[i < QL ? 0 : i - QL];
         };
         // all scores of a block
-        auto score = [&](const uint8_t *kb, f32x16(&sc)[RS][NS]) {
+        auto score = [&](const uint8_t *kb, f32x16(&sc)[NS]) {
             // the LDS addresses are formed anew each block: kept, they cost 8 registers
             int k_at = k_chunk;
             asm volatile("" : "+v"(k_at));
 #pragma unroll
-            for (int x = 0; x < RS; ++x)
+            for (int y = 0; y < NS; ++y)
 #pragma unroll
-                for (int y = 0; y < NS; ++y)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sc[x][y][i] = 0.f;
+                for (int i = 0; i < 16; ++i)
+                    sc[y][i] = 0.f;
             // The LDS reads of the next few products leave before these: left to itself the
             // compiler reads, waits and multiplies one by one.
             u32x4 kf[2][KA];
@@ -414,13 +401,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
 #pragma unroll
                     for (int k = 0; k < KA; ++k) {
                         kf[(g + 1) & 1][k] = read_k(kb, k_at, (g + 1) * KA + k);
-                        ql[(g + 1) & 1][k] = step_q(0, ((g + 1) * KA + k) / NS);
+                        ql[(g + 1) & 1][k] = step_q(((g + 1) * KA + k) / NS);
                     }
                 __builtin_amdgcn_sched_barrier(0);
                 if (g >= 0)
 #pragma unroll
                     for (int k = 0; k < KA; ++k) {
-                        f32x16 &o = sc[0][(g * KA + k) % NS];
+                        f32x16 &o = sc[(g * KA + k) % NS];
                         o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[g & 1][k]),
                                                                     ql[g & 1][k], o, 0, 0, 0);
                     }
@@ -471,72 +458,57 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
             // scores, weights and products of SB keys at a time: registers allow no more
 #pragma unroll 1
             for (int sub = 0; sub < KB / SB; ++sub) {
-            const int key0 = block0 + sub * SB;
-            if (sees(key0)) {
-                const uint64_t lost = *reinterpret_cast<const uint64_t *>(sm_lost[buf]) >> (sub * (SB / 2));
-                if (lost) {
+                const int key0 = block0 + sub * SB;
+                if (sees(key0)) {
+                    const uint64_t lost = *reinterpret_cast<const uint64_t *>(sm_lost[buf]) >> (sub * (SB / 2));
+                    if (lost) {
 #pragma unroll
-                    for (int q = 0; q < SB / 16; ++q)
-#pragma unroll
-                        for (int x = 0; x < RS; ++x)
-                            bad[x] |= (lost >> (8 * q) & 1) && pos[x] >= key0 + 16 * q && pos[x] - reach <= key0 + 16 * q + 15;
-                }
-                int v_at[2] = {v_base[0], v_base[1]};
-                asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
-                const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
-                const uint8_t *vb = sm_v[buf] + sub * SB * ROWB;
-                {
-                    f32x16 sc[RS][NS];
+                        for (int q = 0; q < SB / 16; ++q)
+                            bad |= (lost >> (8 * q) & 1) && pos >= key0 + 16 * q &&
+                                  pos - reach <= key0 + 16 * q + 15;
+                    }
+                    int v_at[2] = {v_base[0], v_base[1]};
+                    asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
+                    const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
+                    const uint8_t *vb = sm_v[buf] + sub * SB * ROWB;
+                    f32x16 sc[NS];
                     score(sm_k[buf] + sub * SB * ROWB, sc);
 #pragma unroll
-                    for (int x = 0; x < RS; ++x)
-#pragma unroll
-                        for (int y = 0; y < NS; ++y)
-                            settle(sc[x][y]);
+                    for (int y = 0; y < NS; ++y)
+                        settle(sc[y]);
                     if (mixed) {
 #pragma unroll
-                        for (int x = 0; x < RS; ++x)
-#pragma unroll
-                            for (int y = 0; y < NS; ++y)
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const int back =
-                                        pos[x] - (key0 + y * 32 + 8 * (i >> 2) + 4 * hh + (i & 3));
-                                    if (back < 0 || back > reach)
-                                        sc[x][y][i] = neg_inf();
-                                }
-                    }
-                    float top[RS];
-                    bool raise = false;
-#pragma unroll
-                    for (int x = 0; x < RS; ++x) {
-                        top[x] = sc[x][0][0];
-#pragma unroll
                         for (int y = 0; y < NS; ++y)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                top[x] = fmaxf(top[x], sc[x][y][i]);
-                        top[x] = fmaxf(top[x], __shfl_xor(top[x], 32)) * scale;
-                        raise |= top[x] > m[x] + 8.0f;
+                            for (int i = 0; i < 16; ++i) {
+                                const int back =
+                                    pos - (key0 + y * 32 + 8 * (i >> 2) + 4 * hh + (i & 3));
+                                if (back < 0 || back > reach)
+                                    sc[y][i] = neg_inf();
+                            }
                     }
-                    if (__ballot(raise)) {
+                    float top = sc[0][0];
 #pragma unroll
-                        for (int x = 0; x < RS; ++x) {
-                            const float m_new = fmaxf(m[x], top[x]);
-                            const float keep = m_new == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m[x] - m_new);
-                            l[x] *= keep;
+                    for (int y = 0; y < NS; ++y)
 #pragma unroll
-                            for (int a = 0; a < DT; ++a)
-                                acc[x][a] *= keep;
-                            m[x] = m_new;
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            top = fmaxf(top, sc[y][i]);
+                    top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+                    if (__ballot(top > m + 8.0f)) {
+                        const float m_new = fmaxf(m, top);
+                        const float keep = m_new == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
+                        l *= keep;
+#pragma unroll
+                        for (int a = 0; a < DT; ++a)
+                            acc[a] *= keep;
+                        m = m_new;
                     }
                     if (odd) { // uniform: what left v goes to the rows that see it
 #pragma unroll 1
                         for (int j = 0; j < SB && key0 + j < s.L; ++j) {
                             const uint8_t *v = static_cast<const uint8_t *>(p.v_pages) +
                                                cell_of(key0 + j) * (E4M3 ? D : ROWB) + hh * (E4M3 ? 4 : 8);
-                            const int back = pos[0] - (key0 + j);
+                            const int back = pos - (key0 + j);
                             const bool seen = back >= 0 && back <= reach;
 #pragma unroll
                             for (int c = 0; c < DT * 4; ++c) { // four columns of this lane's
@@ -551,14 +523,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                                 for (int i = 0; i < 4; ++i) {
                                     const uint32_t z = (i & 1) ? y[i >> 1] & 0xffff0000u : y[i >> 1] << 16;
                                     if (seen && (z & 0x7f800000u) == 0x7f800000u)
-                                        acc[0][c >> 2][(c & 3) * 4 + i] += __uint_as_float(z);
+                                        acc[c >> 2][(c & 3) * 4 + i] += __uint_as_float(z);
                                 }
                                 __builtin_amdgcn_sched_barrier(0);
                             }
                         }
                     }
                     // weights of 16 keys at a time, and the products with their v beside the next ones
-                    constexpr int VA = D == 256 ? 2 : (DT < 4 ? DT : 4), VG = DT / VA; // products at a time
+                    constexpr int VA = DT < 4 ? DT : 4, VG = DT / VA; // products at a time
                     constexpr int GROUPS = 2 * NS * VG;
                     u32x4 vf[2][VA];
                     auto read_ahead = [&](int g) {
@@ -567,25 +539,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                             const int q = g / VG, a = (g % VG) * VA + k;
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
+                                const uint8_t *from =
+                                    vb + q * 16 * ROWB + (v_at[y] ^ ((a & 3) * 64)) + (a >> 2) * 256;
                                 const u32x2 v2 = __builtin_bit_cast(
-                                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                               (__attribute__((address_space(3))) s16x4 *)(vb + q * 16 * ROWB +
-                                                                                           (v_at[y] ^ ((a & 3) * 64)) +
-                                                                                           (a >> 2) * 256)));
+                                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from));
                                 vf[g & 1][k][2 * y] = v2[0];
                                 vf[g & 1][k][2 * y + 1] = v2[1];
                             }
                         }
                     };
                     uint32_t pw[2][4]; // two groups of weights, bf16 pairs
-                    const float off = m[0] == neg_inf() ? 0.f : -m[0];
+                    const float off = m == neg_inf() ? 0.f : -m;
                     auto weigh = [&](int q, int i0, int i1) { // values i0 .. i1 - 1 of 16 keys' eight
 #pragma unroll
                         for (int i = i0; i < i1; i += 2) {
-                            const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[0][q >> 1][8 * (q & 1) + i], scale, off));
-                            const float e1 =
-                                __builtin_amdgcn_exp2f(fmaf(sc[0][q >> 1][8 * (q & 1) + i + 1], scale, off));
-                            l[0] += e0 + e1;
+                            const int at = 8 * (q & 1) + i;
+                            const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at], scale, off));
+                            const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at + 1], scale, off));
+                            l += e0 + e1;
                             // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and
                             // o is rounded to bf16 in the end
                             pw[q & 1][i >> 1] = pack_bf16(e0, e1);
@@ -605,13 +576,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                             bf16x8, u32x4{pw[q & 1][0], pw[q & 1][1], pw[q & 1][2], pw[q & 1][3]});
 #pragma unroll
                         for (int k = 0; k < VA; ++k) {
-                            f32x16 &o = acc[0][part * VA + k];
-                            o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]), pf, o,
-                                                                        0, 0, 0);
+                            f32x16 &o = acc[part * VA + k];
+                            o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]),
+                                                                        pf, o, 0, 0, 0);
                         }
                     }
                 }
-            }
             }
             if constexpr (E4M3) {
                 if (blk + 1 < end) {
@@ -620,29 +590,25 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
                 }
             }
         }
-#pragma unroll
-        for (int x = 0; x < RS; ++x) {
-            const int row = row0 + 32 * x + n_;
-            l[x] += __shfl_xor(l[x], 32);
-            if (((int)bad[x] | __shfl_xor((int)bad[x], 32)) || s.kind == kNan)
-                l[x] = quiet_nan();
-            if (row >= rows)
-                continue;
+        l += __shfl_xor(l, 32);
+        if (((int)bad | __shfl_xor((int)bad, 32)) || s.kind == kNan)
+            l = quiet_nan();
+        if (row < rows) {
             const int64_t tk = s.first + row / p.G;
             const int head = h * p.G + row % p.G;
             if (whole) {
                 const float vs = E4M3 ? p.v_scale[h] : 1.0f;
-                const float inv = l[x] == 0.f ? 0.f : vs / l[x];
+                const float inv = l == 0.f ? 0.f : vs / l;
                 uint16_t *o = p.out.p + tk * p.out.row + (int64_t)head * p.out.head + 4 * hh;
 #pragma unroll
                 for (int a = 0; a < DT; ++a)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<u32x2 *>(o + a * 32 + 2 * i) =
-                            u32x2{pack_bf16(acc[x][a][i] * inv, acc[x][a][i + 1] * inv),
-                                  pack_bf16(acc[x][a][i + 2] * inv, acc[x][a][i + 3] * inv)};
+                            u32x2{pack_bf16(acc[a][i] * inv, acc[a][i + 1] * inv),
+                                  pack_bf16(acc[a][i + 2] * inv, acc[a][i + 3] * inv)};
                 if (hh == 0 && p.lse)
-                    p.lse[tk * p.H_q + head] = lse_of(m[x], l[x]);
+                    p.lse[tk * p.H_q + head] = lse_of(m, l);
             } else {
                 const int64_t part = ((int64_t)w * 2 + slot) * TR + (row - tile * TR);
                 float *o = p.part_o + part * D + 4 * hh;
@@ -651,10 +617,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_tiles_kernel(AttnParams 
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<f32x4 *>(o + a * 32 + 2 * i) =
-                            f32x4{acc[x][a][i], acc[x][a][i + 1], acc[x][a][i + 2], acc[x][a][i + 3]};
+                            f32x4{acc[a][i], acc[a][i + 1], acc[a][i + 2], acc[a][i + 3]};
                 if (hh == 0) {
-                    p.part_ml[part * 2] = m[x];
-                    p.part_ml[part * 2 + 1] = l[x];
+                    p.part_ml[part * 2] = m;
+                    p.part_ml[part * 2 + 1] = l;
                 }
             }
         }
@@ -754,9 +720,8 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     void *args[] = {&q};
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_plan_kernel), dim3(1), dim3(PT), args, 0,
                                    stream);
-    constexpr int NW = 8;
     if (e == hipSuccess)
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, NW, 8 / NW>),
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3>),
                             dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_join_kernel<D, E4M3>),

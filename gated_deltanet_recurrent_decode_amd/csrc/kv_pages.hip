@@ -48,7 +48,10 @@ __device__ __forceinline__ int scan_exclusive(int v, int *total)
     return before + inc - v;
 }
 
-__device__ __forceinline__ int pages_of(int len, int shift) { return (int)(((int64_t)len + (1 << shift) - 1) >> shift); }
+__device__ __forceinline__ int pages_of(int len, int shift)
+{
+    return (int)(((int64_t)len + (1 << shift) - 1) >> shift);
+}
 
 // owner[r] = the first list entry that names row r, for every row that the list names.
 __device__ __forceinline__ void first_owners(const PageParams &p, const int32_t *rows)

@@ -145,7 +145,8 @@ def test_kv_page_refusals():
         "compact": lambda g: L.kv_page_compact(g, FAKE, FAKE, FAKE, big, None),
     }
     for name, call in moves.items():
-        for bad, st in ((dict(k=None), NULL), (dict(v=None), NULL), (dict(layers=0), SHAPE), (dict(page_bytes=0), SHAPE),
+        for bad, st in ((dict(k=None), NULL), (dict(v=None), NULL), (dict(layers=0), SHAPE),
+                        (dict(page_bytes=0), SHAPE),
                         (dict(layers=2, layer_stride=9 * 4096 - 16), SHAPE), (dict(page_bytes=4088), UNSUPPORTED),
                         (dict(k=FAKE + 8), UNSUPPORTED), (dict(layer_stride=9 * 4096 + 8), UNSUPPORTED)):
             assert call(ctypes.byref(pages(**bad))) == st, (name, bad)
@@ -174,13 +175,16 @@ def test_binding_layouts():
                 (k, v, meta(4, 8, dtype=i32), n, None, None), (k, v, table, meta(5, 1, dtype=i32), None, None),
                 (f8, f8, table, n, None, s), (f8, f8, table, n, s, meta(3, dtype=f32)),
                 (meta(2, 16, 64), meta(2, 16, 64), table, n, None, None),
-                (meta(9, 2, 16, 64, dtype=torch.float16), meta(9, 2, 16, 64, dtype=torch.float16), table, n, None, None)):
+                (k.to(torch.float16), v.to(torch.float16), table, n, None, None)):
         with pytest.raises(ValueError):
             at._cache_layout(*bad)
     assert at._packed_layout(meta(3, dtype=i32), meta(4, dtype=i32)) == 3
     with pytest.raises(ValueError):
         at._packed_layout(meta(3, dtype=i32), meta(3, dtype=i32))
-    assert at._heads_layout(meta(7, 4, 64), "q", 7, None, 64) == 4
+    at._heads_layout(meta(7, 4, 64), "q", 7, 4, 64)
+    assert at._packed_heads(meta(7, 4, 64), "q") == (7, 4)
+    with pytest.raises(ValueError):
+        at._packed_heads(meta(7, 256), "q")
     for bad in (meta(6, 4, 64), meta(7, 3, 64), meta(7, 4, 32), meta(7, 4, 128)[:, :, ::2]):
         with pytest.raises(ValueError):
             at._heads_layout(bad, "q", 7, 4, 64)

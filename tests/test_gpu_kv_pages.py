@@ -279,7 +279,8 @@ def test_a_captured_turn(gdn):
         turn()
     for step in range(5):
         rows = [1 + (8 * step + i) % 39 for i in range(8)]
-        lists = ([rows[0], 1 + 3 * step, 0, 0], rows[:4], [30 - step, 20 + step, 0, 7], rows, [9 + 5 * i for i in range(8)])
+        lists = ([rows[0], 1 + 3 * step, 0, 0], rows[:4], [30 - step, 20 + step, 0, 7], rows,
+                 [9 + 5 * i for i in range(8)])
         for t, x in zip((gone, src, dst, grow, add), lists):
             t.copy_(dev.ints(x))
         torch.cuda.synchronize()
