@@ -21,6 +21,11 @@
 // workgroup.  A workgroup finds its piece from the lengths on the device (a
 // captured step follows its lengths) and finishes what lies whole in it; of a
 // triple that is cut it leaves (o, m, l) in the workspace for the second kernel.
+//
+// What bounds it: reading the cache.  MI355X: 64 sequences of 0.2-8 thousand tokens
+// at 16/4 heads of 256, 1.2 GB, 224 us + 5 us to join (5.3 TB/s); 8 of 40-131
+// thousand e4m3 tokens at 32/4 heads of 128, 0.6 GB, 117 + 6 us (5.1 TB/s); one of
+// 777 tokens 11 + 4 us, a chain of dependent reads (lengths, page numbers, keys).
 
 #include "attn_common.h"
 #include "gdn_internal.h"
