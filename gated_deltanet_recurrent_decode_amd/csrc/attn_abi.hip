@@ -33,7 +33,8 @@ gdn_status check_dims(const gdn_attn_dims &d)
         return GDN_ERR_UNSUPPORTED;
     // positions, grids and row counts in 32 bits
     if ((int64_t)d.table_width * d.page_size > INT32_MAX / 2 || (int64_t)d.T * d.H_q > INT32_MAX / 2 ||
-        (int64_t)d.H_q + 2 * (int64_t)d.H_kv > 65535)
+        (int64_t)d.H_q + 2 * (int64_t)d.H_kv > 65535 ||
+        ((int64_t)d.T * (d.H_q / d.H_kv) / 256 + d.B) * d.H_kv > INT32_MAX / 4)
         return GDN_ERR_SHAPE;
     return GDN_OK;
 }

@@ -38,6 +38,7 @@ struct AttnParams {
     long long *before;          // tiles: units of the call before each entry, and the sum of all
     int32_t *entry;             // tiles: [entries][3] sequence, kv head, tile
     int32_t *count;             // tiles: entries
+    int capacity;               // tiles: entries that the workspace holds
     int block;                  // tiles: keys of a block
 };
 

@@ -574,12 +574,13 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
 {
     AttnParams q = p;
     void *args[] = {&q};
+    const int most = p.max_new * p.G; // rows of a sequence that can be cut
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_rows_kernel<D, E4M3>),
                                    dim3((unsigned)p.workgroups), dim3(NT), args, 0, stream);
-    if (e == hipSuccess)
+    if (e == hipSuccess && most > 0)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_join_kernel<D, E4M3>),
-                            dim3((unsigned)p.workgroups, (unsigned)(p.max_new * p.G < TM ? p.max_new * p.G : TM)),
-                            dim3(JT), args, 0, stream);
+                            dim3((unsigned)p.workgroups, (unsigned)(most < TM ? most : TM)), dim3(JT), args, 0,
+                            stream);
     return e;
 }
 

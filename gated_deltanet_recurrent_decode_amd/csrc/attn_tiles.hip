@@ -153,6 +153,8 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
         }
         int all;
         first_entry[threadIdx.x] = plan_scan(mine, &all);
+        // sequences that overlap have more tiles than the workspace was sized for: left out
+        all = all < p.capacity - entries ? all : p.capacity - entries;
         if (threadIdx.x == 0)
             first_entry[PT] = all;
         __syncthreads();
@@ -714,6 +716,7 @@ size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnP
     if (p) {
         char *at = static_cast<char *>(base);
         p->workgroups = workgroups;
+        p->capacity = (int)entries;
         p->part_o = reinterpret_cast<float *>(at);
         p->part_ml = reinterpret_cast<float *>(at + o);
         p->before = reinterpret_cast<long long *>(at + o + ml);

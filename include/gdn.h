@@ -484,6 +484,10 @@ gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gd
  * range is not inside [0, T] is left as it was, and so are tokens outside
  * [cu_seqlens[0], cu_seqlens[B]).
  *
+ * Precondition, not checked: the sequences' token ranges do not overlap
+ * (cu_seqlens is non-decreasing); which of two shows is not defined, and nothing
+ * outside the arrays is touched.
+ *
  * q [T][H_q][d] and out by their strides; they must not overlap.  lse
  * [T][H_q] fp32.  workspace: attn_paged_workspace_bytes(dims) bytes of device
  * memory, 256-byte aligned, contents of no matter before and after; calls that

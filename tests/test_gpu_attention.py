@@ -259,18 +259,93 @@ def test_a_captured_step_follows_its_lengths(gdn):
         assert torch.equal(eager.view(torch.int16), out.view(torch.int16))
 
 
-def test_pages_past_four_gigabytes(gdn):
+@pytest.mark.parametrize("n", [40, 100])
+@pytest.mark.parametrize("d", [64, 256])
+def test_chunks_that_see_nothing(gdn, d, n):
+    # more new tokens than cached ones, in the kernel of long chunks
+    c = A.Cache([(n, 0), (70, 0)], H_q=8, H_kv=2, d=d, page=16, seed=22)
+    c.kv_len[int(c.row[0])] = n - 33
+    out, lse = both(gdn, c, max_new=100)
+    assert (out[:33] == 0).all() and (lse[:33] == -math.inf).all()
+    c.kv_len[int(c.row[0])] = 0
+    both(gdn, c, max_new=100)
+
+
+@pytest.mark.parametrize("max_new", [0, 3, 99])
+def test_more_new_tokens_than_said(gdn, max_new):
+    c = A.Cache([(100, 20), (2, 50)], H_q=8, H_kv=2, d=64, page=16, seed=23)
+    out, lse = run(gdn, c, max_new=max_new)
+    assert out[:100].isnan().all() and lse[:100].isnan().all()
+    want, _, tol, _ = A.attention(c, 64 ** -0.5)
+    if max_new:
+        A.check(out[100:], want[100:], tol[100:], "out")
+    else:
+        assert out[100:].isnan().all()
+
+
+def test_unusable_sequences_among_chunks(gdn):
+    lens = [(100, 40), (80, 30), (90, 20), (300, 10), (60, 60)]
+    c = A.Cache(lens, H_q=4, H_kv=2, d=128, page=16, seed=24)
+    want, want_lse, tol, tol_l = A.attention(c, 128 ** -0.5)
+    row, table, kv_len = c.row.clone(), c.table.clone(), c.kv_len.clone()
+    row[0] = 0
+    row[1] = -3
+    kv_len[int(row[2])] = -1
+    table[int(row[4]), 5] = c.N + 7    # positions 80..95: seen by the tokens from 20 on
+    out, lse = run(gdn, c, row=row, page_table=table, kv_len=kv_len)
+    assert (out[:100] == 0).all() and (lse[:100] == -math.inf).all()
+    assert out[100:270].isnan().all() and lse[100:270].isnan().all()
+    A.check(out[270:590], want[270:590], tol[270:590], "out")
+    A.check(lse[270:590], want_lse[270:590], tol_l[270:590], "lse")
+    assert out[590:].isnan().all() and lse[590:].isnan().all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 0.02])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 90])
+def test_other_scales(gdn, scale, kind, n):
+    c = A.Cache([(n, 77)], H_q=4, H_kv=2, d=128, page=32, kind=kind, seed=25)
+    out, lse = run(gdn, c, scale=scale)
+    o, l, tol, tol_l = A.attention(c, scale)
+    A.check(out, o, tol, "out")
+    A.check(lse, l, tol_l, "lse")
+
+
+def test_overlapping_sequences_touch_nothing_else(gdn):
+    """Ranges that overlap break the precondition; the workspace, sized for ranges that do not, is not overrun."""
+    c = A.Cache([(300, 0)] * 3, H_q=8, H_kv=2, d=64, page=16, seed=26)
+    cu = torch.tensor([0, 300, 10, 300], dtype=torch.int32)
+    c.T, c.q = 300, c.q[:300]
+    need = gdn.attn_paged_workspace_bytes(3, 300, 300, 8, 2, 64)
+    big = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out, lse = run(gdn, c, cu_seqlens=cu, ws=big[:need], max_new=300)
+    assert (big[need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("n", [3, 60])
+def test_pages_past_four_gigabytes(gdn, n):
     """Cells whose byte offsets pass 32 bits: a 5 GiB pool with the sequence at its top."""
     d, H_kv, page = 256, 2, 256
     N = (5 << 30) // (H_kv * page * d * 2)
-    c = A.Cache([(3, 700)], H_q=8, H_kv=H_kv, d=d, page=page, seed=21)
+    c = A.Cache([(n, 700)], H_q=8, H_kv=H_kv, d=d, page=page, seed=21)
     k = torch.zeros(N, H_kv, page, d, dtype=A.BF, device="cuda")
     v = torch.zeros(N, H_kv, page, d, dtype=A.BF, device="cuda")
     up = N - c.N
     k[up:], v[up:] = c.k.cuda(), c.v.cuda()
     table = torch.where(c.table > 0, c.table + up, 0).to(torch.int32).cuda()
     q, out = c.q.cuda(), torch.empty(c.T, 8, d, dtype=A.BF, device="cuda")
-    ws = torch.empty(gdn.attn_paged_workspace_bytes(1, c.T, 3, 8, H_kv, d), dtype=torch.uint8, device="cuda")
-    gdn.attn_paged(q, k, v, table, c.kv_len.cuda(), c.row.cuda(), c.cu.cuda(), out, ws, max_new=3)
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(1, c.T, n, 8, H_kv, d), dtype=torch.uint8, device="cuda")
+    a = table, c.kv_len.cuda(), c.row.cuda(), c.cu.cuda()
+    gdn.attn_paged(q, k, v, *a, out, ws, max_new=n)
     want, _, tol, _ = A.attention(c, d ** -0.5)
     A.check(out, want, tol, "out")
+    # the prologue writes there, and pages move there
+    x = torch.randn(c.T, H_kv, d, device="cuda").to(A.BF)
+    gdn.attn_prologue(None, x, x, None, k, v, *a, None)
+    at = (table[int(c.row[0]), 700 // page].item(), 700 % page)
+    assert torch.equal(k[at[0], :, at[1]], x[0]) and torch.equal(v[at[0], :, at[1]], x[0])
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gdn.kv_page_copy(k, v, torch.tensor([at[0]], **i32), torch.tensor([N - c.N - 2], **i32))
+    torch.cuda.synchronize()
+    assert torch.equal(k[N - c.N - 2].view(torch.int16), k[at[0]].view(torch.int16))
+    assert not k[:N - c.N - 2].any()
