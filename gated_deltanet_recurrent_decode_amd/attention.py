@@ -103,12 +103,15 @@ def _refuse(t, name, dtype, device):
     raise ValueError(f"{name}: must be contiguous")
 
 
-def _gpu(t, name, dtype):
-    """The index of the GPU that `t` is on."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
-        _refuse(t, name, dtype, -1)
-    return t.get_device()
+def _gpu(t, name):
+    """The index of the GPU that `t` is on; the calls below check that everything else is there too."""
+    try:
+        device = t.get_device()
+    except AttributeError:
+        device = -1
+    if device < 0:
+        _refuse(t, name, None, -1)
+    return device
 
 
 def _at(t, name, dtype, device):
@@ -186,13 +189,14 @@ def _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale):
     return N, H_kv, page, d, rows[0], width, kind
 
 
-def _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev):
+def _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch):
     """A layer's cache as the C structure."""
-    torch = _torch()
-    i32, f32 = torch.int32, torch.float32
-    return _CACHE.pack(_at(k_pages, "k_pages", k_pages.dtype, dev), _at(v_pages, "v_pages", v_pages.dtype, dev),
-                       _at_or_none(k_scale, "k_scale", f32, dev), _at_or_none(v_scale, "v_scale", f32, dev),
-                       _at_or_none(page_table, "page_table", i32, dev), _at(kv_len, "kv_len", i32, dev))
+    i32, f32, dtype = torch.int32, torch.float32, k_pages.dtype
+    return _CACHE.pack(_at(k_pages, "k_pages", dtype, dev), _at(v_pages, "v_pages", dtype, dev),
+                       0 if k_scale is None else _at(k_scale, "k_scale", f32, dev),
+                       0 if v_scale is None else _at(v_scale, "v_scale", f32, dev),
+                       0 if page_table is None else _at(page_table, "page_table", i32, dev),
+                       _at(kv_len, "kv_len", i32, dev))
 
 
 def _packed_layout(row, cu_seqlens):
@@ -250,7 +254,7 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
         raise ValueError("q and q_out go together, and so do k and v")
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
     B = _packed_layout(row, cu_seqlens)
-    dev = _gpu(row, "row", i32)
+    dev = _gpu(row, "row")
     hq = ho = hk = hv = rope = norm = None
     H_q = H_kv
     if q is not None:
@@ -263,10 +267,10 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
             raise ValueError("page_table is required to store k and v")
         hk, hv = _heads(k, "k", T, H_kv, d, bf, dev), _heads(v, "v", T, H_kv, d, bf, dev)
     if freqs is not None:
-        if freqs.dim() != 1 or 2 * freqs.shape[0] > d:
+        s = freqs.shape
+        if len(s) != 1 or 2 * s[0] > d:
             raise ValueError("freqs must be [rot/2] with rot <= d")
-        rope = _ROPE.pack(_at(freqs, "freqs", torch.float64, dev), 2 * freqs.shape[0], int(bool(interleaved)),
-                          rope_scale)
+        rope = _ROPE.pack(_at(freqs, "freqs", torch.float64, dev), 2 * s[0], int(bool(interleaved)), rope_scale)
     if q_norm is not None or k_norm is not None:
         for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
             if t is not None and t.shape != (d,):
@@ -277,7 +281,7 @@ def attn_prologue(q, k, v, q_out, k_pages, v_pages, page_table, kv_len, row, cu_
         raise ValueError("positions must be [T]")
     _launch("attn_prologue", lib().attn_prologue, dev, stream,
             _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, 0, 0, kind), hq, hk, hv, ho,
-            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev), _at(row, "row", i32, dev),
+            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
             _at(cu_seqlens, "cu_seqlens", i32, dev), _at_or_none(positions, "positions", i32, dev), rope, norm)
 
 
@@ -306,10 +310,10 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
         raise ValueError("page_table is required")
     if lse is not None and lse.shape != (T, H_q):
         raise ValueError("lse must be [T][H_q]")
-    dev = _gpu(q, "q", bf)
+    dev = _gpu(q, "q")
     _launch("attn_paged", lib().attn_paged, dev, stream,
             _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind), _heads(q, "q", T, H_q, d, bf, dev),
-            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev), _at(row, "row", i32, dev),
+            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
             _at(cu_seqlens, "cu_seqlens", i32, dev), _heads(out, "out", T, H_q, d, bf, dev),
             _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
             _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
@@ -372,7 +376,7 @@ def kv_page_reserve(page_table, kv_len, refs, rows, add, result, workspace, *, p
     i32 = _torch().int32
     R, width, N = _table_layout(page_table, kv_len, refs)
     n = _lists(rows, add, ("rows", "add"))
-    dev = _gpu(page_table, "page_table", i32)
+    dev = _gpu(page_table, "page_table")
     _launch("kv_page_reserve", lib().kv_page_reserve, dev, stream,
             _PAGES.pack(R, width, N, page_size, *_table(page_table, kv_len, refs, dev), 0, 0, 0, 0, 0, 0),
             _at(rows, "rows", i32, dev), _at(add, "add", i32, dev), n, *_scratch(result, workspace, dev))
@@ -388,7 +392,7 @@ def kv_page_fork(k_pages, v_pages, page_table, kv_len, refs, src_rows, dst_rows,
     if N != Np:
         raise ValueError(f"refs counts {N} pages, the cache has {Np}")
     n = _lists(src_rows, dst_rows, ("src_rows", "dst_rows"))
-    dev = _gpu(page_table, "page_table", i32)
+    dev = _gpu(page_table, "page_table")
     _launch("kv_page_fork", lib().kv_page_fork, dev, stream,
             _PAGES.pack(R, width, N, page, *_table(page_table, kv_len, refs, dev), *_pools(k_pages, v_pages, dev),
                         layers, 0, stride, nbytes),
@@ -402,7 +406,7 @@ def kv_page_free(page_table, kv_len, refs, rows, *, stream=None) -> None:
     i32 = _torch().int32
     R, width, N = _table_layout(page_table, kv_len, refs)
     n = _lists(rows, None, ("rows",))
-    dev = _gpu(page_table, "page_table", i32)
+    dev = _gpu(page_table, "page_table")
     _launch("kv_page_free", lib().kv_page_free, dev, stream,
             _PAGES.pack(R, width, N, 16, *_table(page_table, kv_len, refs, dev), 0, 0, 0, 0, 0, 0),
             _at(rows, "rows", i32, dev), n)
@@ -413,7 +417,7 @@ def kv_page_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
     i32 = _torch().int32
     layers, N, page, stride, nbytes = _pages_layout(k_pages, v_pages)
     n = _lists(src, dst, ("src", "dst"))
-    dev = _gpu(src, "src", i32)
+    dev = _gpu(src, "src")
     _launch("kv_page_copy", lib().kv_page_copy, dev, stream,
             _PAGES.pack(1, 1, N, page, 0, 0, 0, *_pools(k_pages, v_pages, dev), layers, 0, stride, nbytes),
             _at(src, "src", i32, dev), _at(dst, "dst", i32, dev), n)
@@ -427,7 +431,7 @@ def kv_page_compact(k_pages, v_pages, page_table, refs, remap, result, workspace
     R, width, N = _table_layout(page_table, None, refs)
     if N != Np or remap.shape != (N,):
         raise ValueError(f"refs and remap must be [{Np}] as the cache has pages")
-    dev = _gpu(page_table, "page_table", i32)
+    dev = _gpu(page_table, "page_table")
     _launch("kv_page_compact", lib().kv_page_compact, dev, stream,
             _PAGES.pack(R, width, N, page, *_table(page_table, None, refs, dev), *_pools(k_pages, v_pages, dev),
                         layers, 0, stride, nbytes),
