@@ -41,6 +41,20 @@ __device__ __forceinline__ void settle(T &x)
     asm volatile("" : "+v"(x));
 }
 
+// The larger of lane i's value and lane i ^ 16's or 32's, by gfx950's row swaps: in the vector
+// unit, where a shuffle goes through LDS.
+__device__ __forceinline__ float max_xor16(float v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float max_xor32(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 enum { kSkip = -1, kNormal = 0, kZero = 1, kNan = 2 };

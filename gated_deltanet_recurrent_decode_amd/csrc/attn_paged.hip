@@ -328,8 +328,7 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
 #pragma unroll
             for (int j = 1; j < 8; ++j)
                 top = fmaxf(top, pr[j]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = max_xor32(max_xor16(top));
             const float m_new = fmaxf(m, top);
             const float m_safe = m_new == neg_inf() ? 0.f : m_new;
             const float keep = __builtin_amdgcn_exp2f(m - m_safe);

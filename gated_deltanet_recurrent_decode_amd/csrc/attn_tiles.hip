@@ -487,6 +487,25 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                     const uint8_t *vb = sm_v[buf] + sub * SB * ROWB;
                     f32x16 sc[NS];
                     score(sm_k[buf] + sub * SB * ROWB, sc);
+                    constexpr int VA = DT < 4 ? DT : 4, VG = DT / VA; // products at a time
+                    constexpr int GROUPS = 2 * NS * VG;
+                    u32x4 vf[2][VA];
+                    auto read_ahead = [&](int g) {
+#pragma unroll
+                        for (int k = 0; k < VA; ++k) {
+                            const int q = g / VG, a = (g % VG) * VA + k;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint8_t *from =
+                                    vb + q * 16 * ROWB + (v_at[y] ^ ((a & 3) * 64)) + (a >> 2) * 256;
+                                const u32x2 v2 = __builtin_bit_cast(
+                                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from));
+                                vf[g & 1][k][2 * y] = v2[0];
+                                vf[g & 1][k][2 * y + 1] = v2[1];
+                            }
+                        }
+                    };
+                    read_ahead(0); // arrives while the maximum is formed
 #pragma unroll
                     for (int y = 0; y < NS; ++y)
                         settle(sc[y]);
@@ -507,7 +526,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             top = fmaxf(top, sc[y][i]);
-                    top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+                    top = max_xor32(top) * scale;
                     if (__ballot(top > m + 8.0f)) {
                         const float m_new = fmaxf(m, top);
                         const float keep = m_new == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -544,24 +563,6 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                         }
                     }
                     // weights of 16 keys at a time, and the products with their v beside the next ones
-                    constexpr int VA = DT < 4 ? DT : 4, VG = DT / VA; // products at a time
-                    constexpr int GROUPS = 2 * NS * VG;
-                    u32x4 vf[2][VA];
-                    auto read_ahead = [&](int g) {
-#pragma unroll
-                        for (int k = 0; k < VA; ++k) {
-                            const int q = g / VG, a = (g % VG) * VA + k;
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint8_t *from =
-                                    vb + q * 16 * ROWB + (v_at[y] ^ ((a & 3) * 64)) + (a >> 2) * 256;
-                                const u32x2 v2 = __builtin_bit_cast(
-                                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from));
-                                vf[g & 1][k][2 * y] = v2[0];
-                                vf[g & 1][k][2 * y + 1] = v2[1];
-                            }
-                        }
-                    };
                     uint32_t pw[2][4]; // two groups of weights, bf16 pairs
                     const float off = m == neg_inf() ? 0.f : -m;
                     auto weigh = [&](int q, int i0, int i1) { // values i0 .. i1 - 1 of 16 keys' eight
@@ -576,7 +577,6 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                             pw[q & 1][i >> 1] = pack_bf16(e0, e1);
                         }
                     };
-                    read_ahead(0);
                     weigh(0, 0, 8);
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
@@ -624,86 +624,91 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                 if (hh == 0 && p.lse)
                     p.lse[tk * p.H_q + head] = lse_of(m, l);
             } else {
-                const int64_t part = ((int64_t)w * 2 + slot) * TR + (row - tile * TR);
-                float *o = p.part_o + part * D + 4 * hh;
+                // as it lies in the registers, 1 KiB a store; the join reads it so
+                const int64_t part = ((int64_t)w * 2 + slot) * NW + wave;
+                float *o = p.part_o + part * 32 * D + lane * 4;
 #pragma unroll
                 for (int a = 0; a < DT; ++a)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<f32x4 *>(o + a * 32 + 2 * i) =
+                        *reinterpret_cast<f32x4 *>(o + a * 1024 + i * 64) =
                             f32x4{acc[a][i], acc[a][i + 1], acc[a][i + 2], acc[a][i + 3]};
                 if (hh == 0) {
-                    p.part_ml[part * 2] = m;
-                    p.part_ml[part * 2 + 1] = l;
+                    p.part_ml[(part * 32 + n_) * 2] = m;
+                    p.part_ml[(part * 32 + n_) * 2 + 1] = l;
                 }
             }
         }
     }
 }
 
-// blockIdx.x = a piece: what begins in it and goes on in the next; a wave a row of it.
+// blockIdx.x = a piece: what begins in it and goes on in the next; a wave 32 rows by 32 columns
+// of it, a lane the 16 values of its row that it had in the registers.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void attn_tiles_join_kernel(AttnParams p)
 {
-    constexpr int E = D / 64, BATCH = 2;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int w0 = blockIdx.x;
+    constexpr int DT = D / 32, BATCH = 2;
+    const int lane = threadIdx.x & 63, n_ = lane & 31, hh = lane >> 5;
+    const int item = uniform(blockIdx.y * 4 + (threadIdx.x >> 6)), wave = item / DT, a = item % DT;
+    // on the XCD that wrote it: some of it is still in its L2
+    const int w0 = (blockIdx.x & 7) * (p.workgroups / 8) + (blockIdx.x >> 3);
     const Cut c = read_cut(p, w0);
     if (c.last < 0)
         return;
     const int w1 = c.last < p.workgroups ? c.last : p.workgroups - 1, slot0 = c.slot, h = c.h;
-    for (int rr = blockIdx.y * 4 + wave; rr < TR; rr += gridDim.y * 4) {
-        const int row = c.tile * TR + rr;
-        if (row >= c.rows)
-            break;
-        auto part_of = [&](int w) { return ((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * TR + rr; };
-        float m = neg_inf(), l = 0.f, o[E];
+    const int row = c.tile * TR + wave * 32 + n_;
+    if (row >= c.rows)
+        return;
+    float m = neg_inf(), l = 0.f;
+    f32x4 o[4];
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            o[i] = 0.f;
-        for (int w = w0; w <= w1; w += BATCH) {
-            float pm[BATCH], pl[BATCH], po[BATCH][E];
+    for (int i = 0; i < 4; ++i)
+        o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int w = w0; w <= w1; w += BATCH) {
+        f32x2 ml[BATCH];
+        f32x4 po[BATCH][4];
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int64_t part = part_of(w + k <= w1 ? w + k : w);
-                pm[k] = p.part_ml[part * 2];
-                pl[k] = p.part_ml[part * 2 + 1];
+        for (int k = 0; k < BATCH; ++k) {
+            const int at = w + k <= w1 ? w + k : w;
+            const int64_t part = ((int64_t)at * 2 + (at == w0 ? slot0 : 0)) * NW + wave;
+            ml[k] = *reinterpret_cast<const f32x2 *>(p.part_ml + (part * 32 + n_) * 2);
 #pragma unroll
-                for (int i = 0; i < E; ++i)
-                    po[k][i] = p.part_o[part * D + i * 64 + lane];
-            }
-            float top = m;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                top = fmaxf(top, pm[k]);
-            const float safe = top == neg_inf() ? 0.f : top;
-            const float keep = __builtin_amdgcn_exp2f(m - safe);
-            l *= keep;
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                o[i] *= keep;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                if (w + k <= w1) {
-                    const float f = __builtin_amdgcn_exp2f(pm[k] - safe);
-                    l = fmaf(pl[k], f, l);
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        o[i] = fmaf(po[k][i], f, o[i]);
-                }
-            }
-            m = top;
+            for (int i = 0; i < 4; ++i)
+                po[k][i] = *reinterpret_cast<const f32x4 *>(p.part_o + part * 32 * D + a * 1024 + i * 256 + lane * 4);
         }
-        const int64_t t = c.first + row / p.G;
-        const int hq = h * p.G + row % p.G;
-        const float vs = E4M3 ? p.v_scale[h] : 1.0f;
-        const float inv = l == 0.f ? 0.f : vs / l;
+        float top = m;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            p.out.p[t * p.out.row + (int64_t)hq * p.out.head + i * 64 + lane] = f32_to_bf16_rne(o[i] * inv);
-        if (lane == 0 && p.lse)
-            p.lse[t * p.H_q + hq] = lse_of(m, l);
+        for (int k = 0; k < BATCH; ++k)
+            top = fmaxf(top, ml[k][0]);
+        const float safe = top == neg_inf() ? 0.f : top;
+        const float keep = __builtin_amdgcn_exp2f(m - safe);
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            if (w + k <= w1) {
+                const float f = __builtin_amdgcn_exp2f(ml[k][0] - safe);
+                l = fmaf(ml[k][1], f, l);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i >> 2][i & 3] = fmaf(po[k][i >> 2][i & 3], f, o[i >> 2][i & 3]);
+            }
+        }
+        m = top;
     }
+    const int64_t t = c.first + row / p.G;
+    const int hq = h * p.G + row % p.G;
+    const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+    const float inv = l == 0.f ? 0.f : vs / l;
+    uint16_t *out = p.out.p + t * p.out.row + (int64_t)hq * p.out.head + a * 32 + 4 * hh;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2 *>(out + 8 * i) =
+            u32x2{pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv)};
+    if (a == 0 && hh == 0 && p.lse)
+        p.lse[t * p.H_q + hq] = lse_of(m, l);
 }
 
 size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnParams *p)
@@ -740,7 +745,7 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
                             dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_join_kernel<D, E4M3>),
-                            dim3((unsigned)p.workgroups, 32), dim3(256), args, 0, stream);
+                            dim3((unsigned)p.workgroups, NW * (D / 32) / 4), dim3(256), args, 0, stream);
     return e;
 }
 
