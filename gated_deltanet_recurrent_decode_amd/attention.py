@@ -135,7 +135,8 @@ def _heads(t, name, T, H, d, dtype, device):
         _heads_layout(t, name, T, H, d)
     if t.dtype is not dtype or t.get_device() != device:
         _refuse(t, name, dtype, device)
-    return _HEADS.pack(t.data_ptr(), step[0], step[1])
+    # the stride of an axis of one says nothing, and torch lets it be anything
+    return _HEADS.pack(t.data_ptr(), step[0] if T > 1 else 0, step[1] if H > 1 else 0)
 
 
 def _launch(name, call, device, stream, *args):

@@ -215,7 +215,8 @@ gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_k
     p.page_shift = page_shift(d.page_size);
     p.width = d.table_width;
     p.max_new = d.max_new;
-    p.window = d.window;
+    // no position lies further back than the table reaches; the kernels add to a window in 32 bits
+    p.window = d.window < (int64_t)d.table_width * d.page_size ? d.window : 0;
     return from_hip(gdn::launch_attn_paged(p, d.d, d.cache_type == 1, stream));
 }
 

@@ -78,8 +78,9 @@ __global__ __launch_bounds__(256) void attn_prologue_kernel(AttnPrologueParams p
     int pos = 0;
     int64_t cell = 0; // the token's place in a page of its own head 0
     if (kind == 0) {
-        pos = p.kv_len[r] - (p.cu[lo + 1] - t);
-        if (pos < 0 || (nkv && pos >= (p.width << p.page_shift))) {
+        const int len = p.kv_len[r];
+        pos = len - (p.cu[lo + 1] - t);
+        if (len < 0 || pos < 0 || (nkv && pos >= (p.width << p.page_shift))) {
             kind = 2;
         } else if (nkv) {
             const int page = p.page_table[(int64_t)r * p.width + (pos >> p.page_shift)];

@@ -369,7 +369,8 @@ gdn_status gdn_slot_copy(const gdn_dims *dims, float *state, gdn_bf16 *conv_stat
  * kv_len[row] - n_b + i.  Every n_b may differ: single decoding tokens, drafted
  * tokens and prompt chunks go in one call.
  *
- * gdn_attn_dims
+ * gdn_attn_dims (GDN_ERR_SHAPE past these: T*H_q and table_width*page_size below
+ * 2^30, H_q + 2 H_kv up to 65535)
  *   B  sequences (0: nothing to do);  T  packed new tokens;  R  rows of the
  *   page table;  H_q, H_kv  heads, H_q a multiple of H_kv: query head h reads
  *   kv head h / (H_q / H_kv);  d  head dim, 64, 128 or 256;  N  pages with the
@@ -459,7 +460,10 @@ gdn_status gdn_rope_freqs(int32_t rot, double base, int32_t stretch, double fact
  * q_out and writes nothing.  Tokens before cu_seqlens[0] or from
  * cu_seqlens[B] on are left as they were.
  * Preconditions, not checked: cu_seqlens is non-decreasing; no two tokens share
- * a cell.  H_q, H_kv, d up to H_q + 2 H_kv <= 65535.
+ * a cell.  max_new and window are not used.
+ * GDN_ERR_NULL, GDN_ERR_SHAPE (sizes; rot odd or past d; scale, eps or add not
+ * finite, eps negative), GDN_ERR_UNSUPPORTED (d, page_size, cache_type,
+ * alignment).
  */
 gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
                          const gdn_heads *q_out, const gdn_kv_cache *cache, const int32_t *row,
@@ -519,6 +523,9 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * (bytes; page_bytes a multiple of 16, v likewise, both 16-byte aligned).
  * Preconditions, not checked: tables, lengths and refs agree.  Entries outside
  * [1, N) are skipped.
+ * GDN_ERR_NULL; GDN_ERR_SHAPE: a size below 1, N above 2^20 where refs are
+ * used, n outside [0, 65535] (kv_page_copy: below 0), layers that overlap, a
+ * workspace too small; GDN_ERR_UNSUPPORTED: page_size, alignment.
  */
 typedef struct gdn_pages {
     int32_t R, table_width, N, page_size;

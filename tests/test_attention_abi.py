@@ -208,3 +208,11 @@ def test_binding_refuses_cpu_tensors_and_missing_parts():
         gdn.attn_prologue(q, None, None, None, c, c, i(2, 2), i(2), i(1), i(2), None)
     with pytest.raises(ValueError, match="GPU tensor"):
         gdn.kv_page_free(i(2, 2), i(2), i(3), i(1))
+
+
+def test_the_stride_of_an_axis_of_one_does_not_matter():
+    bf = torch.bfloat16
+    one = torch.zeros(4, 64, 1, dtype=bf).permute(2, 0, 1)     # one token, its stride 1
+    assert one.stride(0) % 8 and at._HEADS.unpack(at._heads(one, "q", 1, 4, 64, bf, -1))[1:] == (0, 64)
+    one = torch.zeros(4, 64, dtype=bf).as_strided((4, 1, 64), (64, 3, 1))  # one head
+    assert at._HEADS.unpack(at._heads(one, "k", 4, 1, 64, bf, -1))[1:] == (64, 0)

@@ -349,3 +349,35 @@ def test_pages_past_four_gigabytes(gdn, n):
     torch.cuda.synchronize()
     assert torch.equal(k[N - c.N - 2].view(torch.int16), k[at[0]].view(torch.int16))
     assert not k[:N - c.N - 2].any()
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_a_window_longer_than_any_context(gdn, n):
+    """The largest windows see what no window sees, also where the first tokens stand before position 0."""
+    c = A.Cache([(n, 0), (1, 40)], H_q=8, H_kv=2, d=64, page=16, seed=27)
+    c.kv_len[int(c.row[0])] = n - 3
+    want, want_lse = both(gdn, c)
+    for window in (c.width * c.page, 2 ** 30, 2 ** 31 - 1):
+        out, lse = run(gdn, c, window=window)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse), window
+
+
+def test_two_calls_at_once(gdn):
+    """Calls on two streams with a workspace each, of both kernels, do not disturb one another."""
+    cases = [A.Cache([(1, 3000)] * 4, H_q=8, H_kv=2, d=128, page=16, seed=28),
+             A.Cache([(200, 700)], H_q=8, H_kv=2, d=128, page=16, seed=29)]
+    want = [run(gdn, c) for c in cases]
+    calls = []
+    for c in cases:
+        most = max(n for n, _ in c.lens)
+        ws = torch.empty(gdn.attn_paged_workspace_bytes(c.B, c.T, most, 8, 2, 128), dtype=torch.uint8, device="cuda")
+        calls.append((c.cuda(), c.q.cuda(), torch.zeros(c.T, 8, 128, dtype=A.BF, device="cuda"), ws, most))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for (a, q, out, ws, most), s in zip(calls, streams):
+            gdn.attn_paged(q, a["k_pages"], a["v_pages"], a["page_table"], a["kv_len"], a["row"], a["cu_seqlens"],
+                           out, ws, max_new=most, stream=s)
+    torch.cuda.synchronize()
+    for (_, _, out, _, _), (o, _) in zip(calls, want):
+        assert torch.equal(out, o)

@@ -197,6 +197,22 @@ def test_padding_unusable_and_outside_tokens(gdn):
     assert not kp[0].isfinite().any(), "the null page was written"
 
 
+def test_lengths_far_below_zero(gdn):
+    """A length whose distance to the tokens passes 32 bits is a negative position like any other."""
+    c = A.Cache([(3, 10), (1, 5)], H_q=4, H_kv=2, d=64, page=16, seed=8)
+    kv_len = c.kv_len.clone()
+    kv_len[int(c.row[0])] = -2 ** 31
+    a = c.cuda(kv_len=kv_len)
+    q, k, v = split(c, inputs(c).cuda())
+    freqs = gdn.rope_freqs(64, 10000.0)
+    for kk, vv, table in ((k, v, a["page_table"]), (None, None, None)):
+        out = torch.full((c.T, 4, 64), 7.0, dtype=A.BF, device="cuda")
+        gdn.attn_prologue(q, kk, vv, out, a["k_pages"], a["v_pages"], table, a["kv_len"], a["row"], a["cu_seqlens"],
+                          freqs)
+        torch.cuda.synchronize()
+        assert out[:3].isnan().all() and out[3].isfinite().all()
+
+
 def test_a_captured_prologue_follows_its_lengths(gdn):
     c = A.Cache([(1, 10), (1, 47), (1, 0)], H_q=4, H_kv=2, d=128, page=16, seed=7, width=8)
     freqs = gdn.rope_freqs(64, 10000.0, device="cpu")
