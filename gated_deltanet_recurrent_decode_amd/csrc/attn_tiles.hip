@@ -505,7 +505,8 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                             }
                         }
                     };
-                    read_ahead(0); // arrives while the maximum is formed
+                    if (D == 256)
+                        read_ahead(0); // arrives while the maximum is formed
 #pragma unroll
                     for (int y = 0; y < NS; ++y)
                         settle(sc[y]);
@@ -577,6 +578,8 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                             pw[q & 1][i >> 1] = pack_bf16(e0, e1);
                         }
                     };
+                    if (D != 256)
+                        read_ahead(0);
                     weigh(0, 0, 8);
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
