@@ -355,7 +355,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 
         const int end = span.hi > span.lo ? blk1 : blk0; // no keys: nothing to walk
         auto note = [&](int key0, int slot, int id) { // whether the wave's keys have a usable page
-            if (lane == 0)
+            if (lane == 0 && my_row % 16 == 0) // of a part's waves the first: its keys are there if any are
                 sm_lost[slot][my_row >> 4] = !(id > 0 && id < p.N) && key0 + my_row < s.L;
         };
         __syncthreads(); // the buffers of the piece before are read

@@ -143,6 +143,23 @@ def test_a_bad_page_behind_the_window_or_later_does_not_show(gdn):
     assert out[4:].isnan().all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("last", [1, 5, 12, 16])
+@pytest.mark.parametrize("n", [4, 40])
+def test_a_bad_last_page_of_few_cells(gdn, d, kind, last, n):
+    """A page outside the pool that holds only the last few keys: the tokens that see it get NaN, no other."""
+    c = A.Cache([(n, 96 + last - n)], H_q=8, H_kv=2, d=d, page=16, kind=kind, seed=30)
+    table = c.table.clone()
+    table[int(c.row[0]), 6] = c.N
+    out, lse = run(gdn, c, page_table=table, max_new=40)
+    see = min(n, last)
+    assert out[n - see:].isnan().all() and lse[n - see:].isnan().all()
+    want, want_lse, tol, tol_l = A.attention(c, d ** -0.5)
+    A.check(out[:n - see], want[:n - see], tol[:n - see], "out")
+    A.check(lse[:n - see], want_lse[:n - see], tol_l[:n - see], "lse")
+
+
 def test_rows_outside_the_sequences_stay(gdn):
     c = A.Cache([(2, 40), (3, 30)], H_q=4, H_kv=2, d=64, page=16, seed=14)
     cu = c.cu + 4
