@@ -50,6 +50,7 @@ constexpr int PT = 1024; // the planning workgroup
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
 // What a tile of a sequence sees: keys lo .. hi - 1, in blocks from lo on.
 struct Span {
@@ -81,9 +82,9 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s)
 // because the compiler, given the builtin, waits for it before any read of LDS: the loads of the
 // next block would be waited for before this one is worked on.  Whoever reads `to` waits for
 // vmcnt(0) and a barrier first.
-__device__ __forceinline__ void load_to_lds(uint8_t *to, const uint8_t *base, int off)
+__device__ __forceinline__ void load_to_lds(lds_byte *to, const uint8_t *base, int off)
 {
-    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
+    const uint32_t at = (uint32_t)(uintptr_t)to;
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)at)), "v"(off),
                  "s"(base)
                  : "memory"); // m0 is reserved: whatever of the compiler's own needs it sets it first
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
         bf16x8 qf[ST - QL];
         float m = neg_inf(), l = 0.f;
         f32x16 acc[DT];
-        bool bad = false;
+        int bad = 0;
         const int r = row < rows ? row : rows - 1; // rows past the last do as it does, unseen
         const uint16_t *qp = p.q.p + (int64_t)(s.first + r / p.G) * p.q.row +
                              (int64_t)(h * p.G + r % p.G) * p.q.head + hh * 8;
@@ -322,7 +323,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                    ((key0 + my_row) & inside);
         };
         // bf16: k or v of a block into LDS, 1 KiB an instruction
-        auto stage = [&](const void *pages, uint8_t *to, int key0, int id) {
+        auto stage = [&](const void *pages, lds_byte *to, int key0, int id) {
             constexpr int RP = 64 / CH; // rows of an instruction
             const uint8_t *from = static_cast<const uint8_t *>(pages) + first_cell(key0, id) * ROWB;
 #pragma unroll
@@ -368,8 +369,8 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
         int id = 0; // page of the block that is staged next
         auto bring = [&](int key0, int buf) {
             note(key0, buf, id);
-            stage(p.k_pages, sm_k[buf], key0, id);
-            stage(p.v_pages, sm_v[buf], key0, id);
+            stage(p.k_pages, (lds_byte *)sm_k + buf * (KB * ROWB), key0, id);
+            stage(p.v_pages, (lds_byte *)sm_v + buf * (KB * ROWB), key0, id);
             id = next_page(key0 + KB);
         };
         auto bring_e4m3 = [&](int key0, int buf) {
@@ -474,13 +475,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
             for (int sub = 0; sub < KB / SB; ++sub) {
                 const int key0 = block0 + sub * SB;
                 if (sees(key0)) {
-                    const uint64_t lost = *reinterpret_cast<const uint64_t *>(sm_lost[buf]) >> (sub * (SB / 2));
-                    if (lost) {
-#pragma unroll
-                        for (int q = 0; q < SB / 16; ++q)
-                            bad |= (lost >> (8 * q) & 1) && pos >= key0 + 16 * q &&
-                                  pos - reach <= key0 + 16 * q + 15;
-                    }
+                    uint32_t lost = *reinterpret_cast<const uint32_t *>(&sm_lost[buf][sub * (SB / 16)]);
                     int v_at[2] = {v_base[0], v_base[1]};
                     asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
                     const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
@@ -510,6 +505,15 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 #pragma unroll
                     for (int y = 0; y < NS; ++y)
                         settle(sc[y]);
+                    asm volatile("" : "+v"(lost)); // waited for here, not before the scores
+                    if (__ballot(lost != 0)) {
+#pragma unroll
+                        for (int q = 0; q < SB / 16; ++q)
+                            bad |= (lost >> (8 * q) & 1) && pos >= key0 + 16 * q &&
+                                           pos - reach <= key0 + 16 * q + 15
+                                       ? 1
+                                       : 0;
+                    }
                     if (mixed) {
 #pragma unroll
                         for (int y = 0; y < NS; ++y)
@@ -521,12 +525,15 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                                     sc[y][i] = neg_inf();
                             }
                     }
-                    float top = sc[0][0];
+                    float tops[NS]; // a chain each
 #pragma unroll
-                    for (int y = 0; y < NS; ++y)
+                    for (int y = 0; y < NS; ++y) {
+                        tops[y] = sc[y][0];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            top = fmaxf(top, sc[y][i]);
+                        for (int i = 1; i < 16; ++i)
+                            tops[y] = fmaxf(tops[y], sc[y][i]);
+                    }
+                    float top = NS == 2 ? fmaxf(tops[0], tops[NS - 1]) : tops[0];
                     top = max_xor32(top) * scale;
                     if (__ballot(top > m + 8.0f)) {
                         const float m_new = fmaxf(m, top);
@@ -608,7 +615,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
             }
         }
         l += __shfl_xor(l, 32);
-        if (((int)bad | __shfl_xor((int)bad, 32)) || s.kind == kNan)
+        if ((bad | __shfl_xor(bad, 32)) || s.kind == kNan)
             l = quiet_nan();
         if (row < rows) {
             const int64_t tk = s.first + row / p.G;
