@@ -476,6 +476,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                 const int key0 = block0 + sub * SB;
                 if (sees(key0)) {
                     uint32_t lost = *reinterpret_cast<const uint32_t *>(&sm_lost[buf][sub * (SB / 16)]);
+                    __builtin_amdgcn_s_setprio(0);
                     int v_at[2] = {v_base[0], v_base[1]};
                     asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
                     const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
@@ -525,6 +526,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                                     sc[y][i] = neg_inf();
                             }
                     }
+                    __builtin_amdgcn_s_setprio(1);
                     float tops[NS]; // a chain each
 #pragma unroll
                     for (int y = 0; y < NS; ++y) {
