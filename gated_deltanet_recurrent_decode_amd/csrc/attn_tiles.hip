@@ -526,7 +526,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                                     sc[y][i] = neg_inf();
                             }
                     }
-                    __builtin_amdgcn_s_setprio(1);
+                    __builtin_amdgcn_s_setprio(2);
                     float tops[NS]; // a chain each
 #pragma unroll
                     for (int y = 0; y < NS; ++y) {
@@ -590,6 +590,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                     if (D != 256)
                         read_ahead(0);
                     weigh(0, 0, 8);
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
                         const int q = g / VG, part = g % VG;
