@@ -313,7 +313,8 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
         raise ValueError("lse must be [T][H_q]")
     dev = _gpu(q, "q")
     _launch("attn_paged", lib().attn_paged, dev, stream,
-            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind), _heads(q, "q", T, H_q, d, bf, dev),
+            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind),
+            _heads(q, "q", T, H_q, d, bf, dev),
             _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
             _at(cu_seqlens, "cu_seqlens", i32, dev), _heads(out, "out", T, H_q, d, bf, dev),
             _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
