@@ -592,9 +592,12 @@ hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t s
     return e4m3 ? launch_de<256, true>(p, stream) : launch_de<256, false>(p, stream);
 }
 
-// Up to this many rows a sequence the kernel of 16-row tiles is used: it reads a
-// sequence's keys once per tile, the other once for 256 rows but through LDS.
-constexpr int kFewRows = 64;
+// Up to one tile of rows a sequence this kernel is used: it reads a sequence's keys once per 16
+// rows, the other (attn_tiles.hip) once for 256, but through LDS and with a third launch.  Rows
+// here / there in us, bf16: 64 sequences over 2-4 thousand tokens, 32/4 heads of 128: 8 rows 82 / 87,
+// 32 rows 135 / 95, 64 rows 247 / 105; 12 over 2-4 thousand, 16/2 heads of 256: 8 rows 35 / 38,
+// 32 rows 52 / 39; 8 over 0.5-1 thousand, 32/8 heads of 64: 16 rows 18 / 22, 32 rows 20 / 22.
+constexpr int kFewRows = 16;
 
 size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)
 {
