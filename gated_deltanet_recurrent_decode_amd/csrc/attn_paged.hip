@@ -162,7 +162,7 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
         const long long v = u - before;
         const long long ht = quotient(v, s.units);
         const int unit0 = (int)(v - ht * s.units);
-        const int h = (int)quotient(ht, s.tiles), tile = (int)(ht - (long long)h * s.tiles);
+        const int h = uniform((int)quotient(ht, s.tiles)), tile = uniform((int)(ht - (long long)h * s.tiles));
         const long long t0 = before + ht * s.units, t1 = t0 + s.units;
         const long long e = t1 < u_end ? t1 : u_end;
         const int unit1 = unit0 + (int)(e - u);
@@ -203,14 +203,18 @@ __global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
         bool bad = false;
         const float scale = E4M3 ? p.scale * p.k_scale[h] : p.scale;
 
-        const int k_end = s.lo + unit1 * UNIT < s.L ? s.lo + unit1 * UNIT : s.L;
-        for (int key0 = s.lo + unit0 * UNIT + wave * 32; key0 < k_end; key0 += UNIT) {
+        const int k_end = uniform(s.lo + unit1 * UNIT < s.L ? s.lo + unit1 * UNIT : s.L);
+        auto *tab = (__attribute__((address_space(4))) const int32_t *)(p.page_table + (int64_t)uniform(s.r) * p.width);
+        auto page_of = [&](int key) { return key < k_end ? tab[key >> p.page_shift] : 0; };
+        const int key_first = uniform(s.lo + unit0 * UNIT + wave * 32);
+        int next[2] = {page_of(key_first), page_of(key_first + 16)};
+        for (int key0 = key_first; key0 < k_end; key0 += UNIT) {
+            int page[2] = {next[0], next[1]};
+            // the next block's page numbers, while this one is worked on
+            next[0] = page_of(key0 + UNIT);
+            next[1] = page_of(key0 + UNIT + 16);
             if (key0 > max_pos || (p.window > 0 && key0 + 31 <= min_pos - p.window))
                 continue; // no row of the tile sees the block
-            int page[2];
-            const int32_t *tab = p.page_table + (int64_t)s.r * p.width;
-            page[0] = tab[key0 >> p.page_shift];
-            page[1] = key0 + 16 < s.L ? tab[(key0 + 16) >> p.page_shift] : 0;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (page[t] < 1 || page[t] >= p.N) { // uniform
