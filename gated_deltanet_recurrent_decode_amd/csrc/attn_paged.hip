@@ -124,7 +124,7 @@ __device__ __forceinline__ Place locate(const AttnParams &p, Hit hit)
 // D = 64, 128 or 256.  A lane owns EV consecutive columns of v in each of NH
 // 128-column parts (D = 64: four columns of one part).
 template <int D, bool E4M3>
-__global__ __launch_bounds__(NT) void attn_rows_kernel(AttnParams p)
+__global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p)
 {
     constexpr int EV = D == 64 ? 4 : 8, NH = D / (16 * EV), NS = D / 32;
     constexpr int LD = D + 4; // LDS row, padded against bank conflicts
