@@ -65,14 +65,50 @@ struct Place {
     RowSeq s;
 };
 
+__device__ __forceinline__ long long lane_of(long long v, int lane)
+{
+    const uint32_t lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+    return (long long)((uint64_t)hi << 32 | lo);
+}
+
 // Where the line of units holds what `hit` asks for (a predicate of a sequence,
-// its first unit, its units and the units of the call).  TH threads.
+// its first unit, its units and the units of the call).  TH threads; up to 64
+// sequences each wave for itself, with no barrier.
 template <int TH, class Hit>
 __device__ __forceinline__ Place locate(const AttnParams &p, Hit hit)
 {
     __shared__ long long wave_sum[TH / 64];
     __shared__ Place found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (p.B <= 64) {
+        RowSeq s{};
+        long long u = 0;
+        if (lane < p.B) {
+            s = read_row_seq(p, lane);
+            u = seq_units(p, s);
+        }
+        long long inc = u;
+        for (int m = 1; m < p.B; m <<= 1) {
+            const long long o = __shfl_up(inc, m);
+            if (lane >= m)
+                inc += o;
+        }
+        Place f;
+        f.total = lane_of(inc, p.B - 1);
+        const uint64_t where = __ballot(u > 0 && hit(s, inc - u, u, f.total));
+        const int k = where ? __builtin_ctzll(where) : 0;
+        f.b = where ? k : -1;
+        f.before = lane_of(inc - u, k);
+        f.s.kind = __builtin_amdgcn_readlane(s.kind, k);
+        f.s.first = __builtin_amdgcn_readlane(s.first, k);
+        f.s.n = __builtin_amdgcn_readlane(s.n, k);
+        f.s.L = __builtin_amdgcn_readlane(s.L, k);
+        f.s.lo = __builtin_amdgcn_readlane(s.lo, k);
+        f.s.r = __builtin_amdgcn_readlane(s.r, k);
+        f.s.tiles = __builtin_amdgcn_readlane(s.tiles, k);
+        f.s.units = __builtin_amdgcn_readlane(s.units, k);
+        return f;
+    }
     long long total = 0;
     if (tid == 0)
         found.b = -1;
