@@ -23,9 +23,13 @@
 // triple that is cut it leaves (o, m, l) in the workspace for the second kernel.
 //
 // What bounds it: reading the cache.  MI355X: 64 sequences of 0.2-8 thousand tokens
-// at 16/4 heads of 256, 1.2 GB, 224 us + 5 us to join (5.3 TB/s); 8 of 40-131
-// thousand e4m3 tokens at 32/4 heads of 128, 0.6 GB, 117 + 6 us (5.1 TB/s); one of
-// 777 tokens 11 + 4 us, a chain of dependent reads (lengths, page numbers, keys).
+// at 16/4 heads of 256, 1.2 GB, 223 us a call (5.35 TB/s); 8 of 40-131 thousand e4m3
+// tokens at 32/4 heads of 128, 0.6 GB, 114 us (5.24 TB/s), 6 of them to join; one of 777
+// tokens 13 us, 11 + 4 alone, a chain of dependent reads (lengths, page numbers, keys).
+// What gave most after the layouts: page numbers read a block ahead by the scalar unit
+// (239 -> 228 us at the first size), the search within a wave (230 -> 225).  At 256
+// columns one workgroup a CU at a time with more registers is faster than two (230
+// against 235), at 128 two (110 -> 109).
 
 #include "attn_common.h"
 #include "gdn_internal.h"
