@@ -36,8 +36,8 @@ struct AttnParams {
     int B, T, R, H_q, H_kv, G, N, page_shift, width, max_new, window;
     int workgroups;
     long long *before;          // tiles: units of the call before each entry, and the sum of all
-    int32_t *entry;             // tiles: [entries][3] sequence, kv head, tile
-    int32_t *count;             // tiles: entries
+    int32_t *entry;             // tiles: [entries][8] kv head, tile, the sequence
+    int32_t *count;             // tiles: entries, and from [2] on their units in 64 bits
     int capacity;               // tiles: entries that the workspace holds
     int block;                  // tiles: keys of a block
 };

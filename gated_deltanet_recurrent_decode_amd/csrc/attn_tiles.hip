@@ -53,9 +53,12 @@ constexpr int block_keys(int d) { return d == 256 ? 32 : 128; }
 constexpr int NW = TR / 32; // waves
 constexpr int NT = 64 * NW;
 constexpr int PT = 1024; // the planning workgroup
+// what the plan says of an entry: kv head, tile, and its sequence, so that nobody reads the lengths again
+constexpr int kEntry = 8;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -170,6 +173,7 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
             const int e = e0 + threadIdx.x;
             long long u = 0;
             int q = 0, h = 0, tile = 0;
+            Seq s{};
             if (e < all) {
                 int lo = 0, hi = PT; // the last sequence with first_entry <= e
                 while (hi - lo > 1) {
@@ -180,7 +184,7 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
                         hi = mid;
                 }
                 q = lo;
-                const Seq s = seqs[q];
+                s = seqs[q];
                 const int tiles = tiles_of(p, s), x = e - first_entry[q];
                 h = x / tiles;
                 tile = x - h * tiles;
@@ -191,9 +195,9 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
             if (e < all) {
                 const int64_t o = entries + e;
                 p.before[o] = at;
-                p.entry[o * 3] = b0 + q;
-                p.entry[o * 3 + 1] = h;
-                p.entry[o * 3 + 2] = tile;
+                i32x4 *to = reinterpret_cast<i32x4 *>(p.entry + o * kEntry);
+                to[0] = i32x4{h, tile, s.kind, s.first};
+                to[1] = i32x4{s.n, s.L, s.r, 0};
             }
             units += sum;
         }
@@ -202,6 +206,7 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
     if (threadIdx.x == 0) {
         p.before[entries] = units;
         *p.count = entries;
+        *reinterpret_cast<long long *>(p.count + 2) = units;
     }
 }
 
@@ -227,7 +232,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
     const int count = *p.count;
-    const long long total = p.before[count];
+    const long long total = *reinterpret_cast<const long long *>(p.count + 2);
     // consecutive pieces on one XCD (workgroups go round the eight): they share keys in its L2
     const int per = p.workgroups / 8;
     const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -256,10 +261,10 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
     }
 
     while (u < u_end) {
-        const int b = uniform(p.entry[(int64_t)e * 3]), h = uniform(p.entry[(int64_t)e * 3 + 1]),
-                  tile = uniform(p.entry[(int64_t)e * 3 + 2]);
+        const int32_t *entry = p.entry + (int64_t)e * kEntry;
+        const int h = uniform(entry[0]), tile = uniform(entry[1]);
+        const Seq s{uniform(entry[2]), uniform(entry[3]), uniform(entry[4]), uniform(entry[5]), 0, uniform(entry[6])};
         const long long t0 = p.before[e], t1 = p.before[e + 1];
-        const Seq s = read_seq(p, b);
         const Span span = span_of(p, s, tile);
         const long long stop = t1 < u_end ? t1 : u_end;
         const int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
@@ -736,7 +741,7 @@ size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnP
     const int workgroups = (device_cus() + 7) / 8 * 8;
     const size_t entries = ((size_t)T * G / TR + B) * H_kv;
     const size_t o = round256((size_t)workgroups * 2 * TR * d * 4), ml = round256((size_t)workgroups * 2 * TR * 2 * 4),
-                 bf = round256((entries + 1) * 8), en = round256(entries * 3 * 4),
+                 bf = round256((entries + 1) * 8), en = round256(entries * kEntry * 4),
                  cut = round256((size_t)workgroups * 8 * 4);
     if (p) {
         char *at = static_cast<char *>(base);

@@ -83,6 +83,19 @@ def test_many_sequences(gdn):
     both(gdn, A.Cache(lens, H_q=2, H_kv=1, d=64, page=16, seed=8))
 
 
+@pytest.mark.parametrize("B", [2, 63, 64, 65, 255, 256, 257, 513])
+def test_sequences_around_every_round_of_the_search(gdn, B):
+    lens = [((i * 5) % 4 > 0, (i * 29) % 300) for i in range(B - 1)] + [(1, 700)]
+    both(gdn, A.Cache([(int(n), p) for n, p in lens], H_q=2, H_kv=2, d=64, page=16, seed=B))
+
+
+@pytest.mark.parametrize("B", [70, 1023, 1024, 1025])
+def test_many_short_chunks(gdn, B):
+    # more than one round of the plan over sequences, some of them empty
+    lens = [((i * 3) % 7, (i * 37) % 60) for i in range(B - 1)] + [(70, 30)]
+    both(gdn, A.Cache(lens, H_q=4, H_kv=1, d=64, page=16, seed=B))
+
+
 def test_large_scores_and_a_dominant_key(gdn):
     c = A.Cache([(3, 200)], H_q=4, H_kv=2, d=128, page=16, seed=9, q_scale=30.0)
     both(gdn, c)
