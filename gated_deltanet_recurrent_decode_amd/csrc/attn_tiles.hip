@@ -23,22 +23,24 @@
 // Work is dealt out by the key: a first kernel lists every (sequence, kv head,
 // tile) with its blocks that the causal mask and the window leave; the line of
 // all blocks is cut into one piece a workgroup, and what is cut is joined by a
-// third kernel (27 us of 213 at 134 MB of parts, which lie in the workspace as they
+// third kernel (26 us of 212 at 134 MB of parts, which lie in the workspace as they
 // lay in the registers: 1 KiB a store).
 //
 // What bounds it: the two waves of a SIMD get their products and their weights
-// overlapped by 40% only (counters: matrix cores busy 52% of the cycles, weights and
+// overlapped by 40% only (counters: matrix cores busy 54% of the cycles, weights and
 // masks 48%, a quarter waiting), because a wave's own work is a chain: scores,
-// maximum, weights, products.  A wave that forms its maximum goes before one with
-// products, and that before one that forms scores (s_setprio: 673 -> 663 us at the
-// first size below).  Tried and slower, at the same size when the kernel took 785 us
-// under the profiler: the next block's scores formed beside these weights (903; 32
-// more registers copied a block), the halves of the workgroup one phase apart by
-// two barriers a block (892) or by the place of a block's one barrier (686 -> 704 us a
-// call), the next block's loads spread between the score products (844), 64 rows a wave
-// and blocks of 64 keys at 256 columns (spills).  MI355X: 4096 + 3001 tokens at 16/2 heads
-// of 128 over 8-12 thousand others 663 us a call, 1006 TFLOP/s; a mixed step of 12
-// sequences at 16/2 heads of 256 213 us, 693 TFLOP/s.
+// maximum, weights, products; and the card's power, for the clock falls to 1.7 GHz.  A
+// wave that forms its maximum goes before one with products, and that before one that
+// forms scores (s_setprio: 673 -> 663 us at the first size below).  Tried and slower, at
+// the same size when the kernel took 785 us under the profiler: the next block's scores
+// formed beside these weights (903; 32 more registers copied a block), the halves of the
+// workgroup one phase apart by two barriers a block (892) or by the place of a block's
+// one barrier (686 -> 704 us a call), the next block's loads spread between the score
+// products (844), two workgroups of 128 rows a CU (1% fewer cycles, but 663 -> 701 us a
+// call: k and v staged twice lower the clock), a step's first LDS reads before the step
+// (the same), 64 rows a wave and blocks of 64 keys at 256 columns (spills).  MI355X:
+// 4096 + 3001 tokens at 16/2 heads of 128 over 8-12 thousand others 663 us a call, 1006
+// TFLOP/s; a mixed step of 12 sequences at 16/2 heads of 256 212 us, 696 TFLOP/s.
 
 #include "attn_common.h"
 #include "gdn_internal.h"
