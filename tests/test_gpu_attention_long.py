@@ -1,0 +1,158 @@
+"""GPU: paged attention where every workgroup walks many blocks of keys, against
+64-bit references with a bound per (token, head) that a lost block exceeds: the
+next block's staging, maxima carried over blocks, entries finished by one
+workgroup, entries cut in a workgroup's first and last place, unusable cells in
+the middle of a piece."""
+import math
+
+import pytest
+import torch
+
+from tests import attn_helpers as A
+from tests import attn_norms as N
+from tests.test_gpu_attention import run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import gated_deltanet_recurrent_decode_amd as m
+    m.lib()
+    return m
+
+
+def workgroups(few):
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    return 2 * cus if few else -(-cus // 8) * 8
+
+
+def pieces(c, window=0):
+    """The work as the kernel that takes this call deals it."""
+    few = max(n for n, _ in c.lens) * (c.H_q // c.H_kv) <= 16
+    return N.deal(c, window, workgroups(few), few)
+
+
+def both(gdn, c, window=0, **kw):
+    out, lse = run(gdn, c, window=window, **kw)
+    o, l, tol, tol_l = N.attention(c, c.d ** -0.5, window, "cuda")
+    N.check_norms(out, o, tol, "out")
+    A.check(lse, l, tol_l, "lse")
+    return out, lse
+
+
+CHUNKS = [(300, 2500), (513, 4000), (1, 777), (700, 1200)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 900])
+def test_chunks_of_many_blocks(gdn, d, kind, window):
+    c = A.Cache(CHUNKS, H_q=16, H_kv=8, d=d, page=32, kind=kind, seed=d + window)
+    work = pieces(c, window)
+    assert min(sum(b - a for _, a, b, _, _ in w) for w in work) > 2
+    assert any(slot == 1 and a == 0 and b < size for w in work for _, a, b, size, slot in w)
+    both(gdn, c, window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_chunks_of_a_few_blocks(gdn, d, kind):
+    """Pieces that hold an entry's end, whole entries of several blocks, and the next one's beginning."""
+    lens = [(20 + (29 * i) % 110, 300 + (37 * i) % 300) for i in range(48)]
+    c = A.Cache(lens, H_q=32, H_kv=8, d=d, page=16, kind=kind, seed=d)
+    work = pieces(c)
+    whole = [w for w in work if any(b - a == size > 2 for _, a, b, size, _ in w)]
+    assert len(whole) > len(work) // 4
+    assert any(len(w) > 2 and w[0][1] > 0 and w[-1][2] < w[-1][3] for w in work)
+    both(gdn, c)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,window", [(1, 0), (4, 0), (1, 1000), (4, 1200)])
+def test_decode_batches_of_many_units(gdn, d, kind, n, window):
+    lens = [(1 + i % n, 900 + (613 * i) % 2500) for i in range(32)]
+    c = A.Cache(lens, H_q=16, H_kv=4, d=d, page=64, kind=kind, seed=n + window)
+    work = pieces(c, window)
+    assert sum(b - a for w in work for _, a, b, _, _ in w) > 2 * len(work)
+    assert any(slot == 1 and a == 0 and b < size for w in work for _, a, b, size, slot in w)
+    both(gdn, c, window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 90])
+def test_a_long_context_over_every_workgroup(gdn, d, kind, n):
+    c = A.Cache([(n, 20011), (1, 9)], H_q=8, H_kv=1, d=d, page=64, kind=kind, seed=5)
+    both(gdn, c)
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_scores_that_rise_and_fall_along_the_keys(gdn, n):
+    """Each block's keys are longer than the last one's, or shorter: the maximum is raised all the way, or once."""
+    c = A.Cache([(n, 6000), (n, 6100)], H_q=8, H_kv=4, d=128, page=64, seed=31)
+    for b, ends in ((0, (0.05, 6.0)), (1, (6.0, 0.05))):
+        r = int(c.row[b])
+        L = int(c.kv_len[r])
+        size = torch.linspace(*ends, L)
+        for t in range(0, L, c.page):
+            m = min(c.page, L - t)
+            c.k[int(c.table[r, t // c.page]), :, :m] *= size[t:t + m, None].to(A.BF)
+    both(gdn, c)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,B", [(4, 40), (300, 12)])
+def test_values_that_are_not_finite_amid_a_piece(gdn, d, kind, n, B):
+    """Some tokens' windows reach the cell and others' do not, blocks after a piece's first and before its last."""
+    window = 700
+    c = A.Cache([(n, 1100 + 17 * i) for i in range(B)], H_q=32, H_kv=8, d=d, page=32, kind=kind, seed=33)
+    work = pieces(c, window)
+    assert max(b - a for w in work for _, a, b, _, _ in w) > 2
+    bad = [math.nan] if kind == "e4m3" else [math.nan, math.inf, -math.inf]
+    for b in range(c.B):
+        r, L = int(c.row[b]), int(c.kv_len[int(c.row[b])])
+        first = L - n - window + 1  # the first token's first position
+        # seen by the first tokens only; and cells between, which every token sees
+        for i, at in enumerate((first + n // 2 - 1, first + n // 2 + 40, first + 350)):
+            if b % 3 == i or i == 0:
+                c.v[int(c.table[r, at // c.page]), b % 8, at % c.page, (7 * b + i) % d] = bad[(b + i) % len(bad)]
+    both(gdn, c, window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,B", [(4, 40), (300, 12)])
+def test_a_bad_page_amid_a_piece(gdn, d, kind, n, B):
+    window = 700
+    c = A.Cache([(n, 1100 + 17 * i) for i in range(B)], H_q=32, H_kv=8, d=d, page=32, kind=kind, seed=34)
+    work = pieces(c, window)
+    assert max(b - a for w in work for _, a, b, _, _ in w) > 2
+    table = c.table.clone()
+    nan = torch.zeros(c.T, dtype=torch.bool)
+    for b in range(c.B):
+        r, L = int(c.row[b]), int(c.kv_len[int(c.row[b])])
+        first = L - n - window + 1
+        at = (first + (n // 2 if b % 2 else 350)) // c.page  # on the first tokens' edge, or between
+        if b % 4 == 3:
+            at = first // c.page - 1                           # behind every window
+        table[r, at] = (c.N, 0, -1, c.N + 5)[b % 4]
+        pos = torch.arange(L - n, L)
+        nan[int(c.cu[b]):int(c.cu[b + 1])] = pos - window + 1 < (at + 1) * c.page
+    assert nan.any() and not nan.all()
+    out, lse = run(gdn, c, window=window, page_table=table)
+    o, l, tol, tol_l = N.attention(c, d ** -0.5, window, "cuda")
+    out, lse = out.cpu(), lse.cpu()
+    assert out[nan].isnan().all() and lse[nan].isnan().all()
+    N.check_norms(out[~nan], o[~nan], tol[~nan], "out")
+    A.check(lse[~nan], l[~nan], tol_l[~nan], "lse")
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_many_blocks_give_the_same_bits_again(gdn, d):
+    c = A.Cache(CHUNKS, H_q=16, H_kv=8, d=d, page=32, seed=35)
+    one, l1 = run(gdn, c)
+    two, l2 = run(gdn, c)
+    assert torch.equal(one.view(torch.int16), two.view(torch.int16)) and torch.equal(l1, l2)
