@@ -164,10 +164,12 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
             seqs[threadIdx.x] = s;
             mine = tiles_of(p, s) * p.H_kv;
         }
-        int all;
-        first_entry[threadIdx.x] = plan_scan(mine, &all);
-        // sequences that overlap have more tiles than the workspace was sized for: left out
-        all = all < p.capacity - entries ? all : p.capacity - entries;
+        // sequences that overlap have more tiles than the workspace was sized for (and than 32 bits
+        // count: 512 of 2^22 in a round): what is past its end is left out
+        long long sum_all;
+        const long long mine_at = plan_scan((long long)mine, &sum_all);
+        const int room = p.capacity - entries, all = sum_all < room ? (int)sum_all : room;
+        first_entry[threadIdx.x] = mine_at < all ? (int)mine_at : all;
         if (threadIdx.x == 0)
             first_entry[PT] = all;
         __syncthreads();
