@@ -103,6 +103,9 @@ gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gd
     gdn_status st = check_dims(d);
     if (st != GDN_OK)
         return st;
+    // a workgroup of 256 threads a token: a launch counts its threads in 32 bits
+    if (d.T > (1 << 24) - 1)
+        return GDN_ERR_SHAPE;
     if (has_kv && (st = check_cache(*cache, d.cache_type == 1)) != GDN_OK)
         return st;
     for (const gdn_heads *h : {q, q_out, k, v})

@@ -461,9 +461,9 @@ gdn_status gdn_rope_freqs(int32_t rot, double base, int32_t stretch, double fact
  * cu_seqlens[B] on are left as they were.
  * Preconditions, not checked: cu_seqlens is non-decreasing; no two tokens share
  * a cell.  max_new and window are not used.
- * GDN_ERR_NULL, GDN_ERR_SHAPE (sizes; rot odd or past d; scale, eps or add not
- * finite, eps negative), GDN_ERR_UNSUPPORTED (d, page_size, cache_type,
- * alignment).
+ * GDN_ERR_NULL, GDN_ERR_SHAPE (sizes, T of 2^24 and more; rot odd or past d;
+ * scale, eps or add not finite, eps negative), GDN_ERR_UNSUPPORTED (d, page_size,
+ * cache_type, alignment).
  */
 gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
                          const gdn_heads *q_out, const gdn_kv_cache *cache, const int32_t *row,
