@@ -301,7 +301,8 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
 
     q and out [T][H_q][d] bf16 by their strides; row [B], cu_seqlens [B+1] int32; workspace a uint8 tensor of
     attn_paged_workspace_bytes; lse [T][H_q] float32 or None; scale defaults to d ** -0.5; no sequence has more
-    than max_new new tokens."""
+    than max_new new tokens.  max_new picks the kernel and with it the precision: with max_new * H_q / H_kv above
+    16 the softmax's weights are rounded to bf16 for the product with v."""
     torch = _torch()
     bf, i32 = torch.bfloat16, torch.int32
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)

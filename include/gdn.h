@@ -477,11 +477,14 @@ gdn_status attn_prologue(const gdn_attn_dims *dims, const gdn_heads *q, const gd
  *   o = sum_j softmax_j(scale * q . k_j) v_j   over the positions
  *   max(0, p - window + 1) <= j <= p           (0 <= j <= p without a window)
  *   lse = log sum_j exp(scale * q . k_j)       (natural; lse may be NULL)
- * q and k enter as they are, scores and the softmax's maximum and sum are fp32,
- * weights are rounded to bf16 for the product with v (fp32 sums), o is rounded
- * once.  A token that sees no position (kv_len < n_b, or a padding sequence on
- * row 0) gets o = +0.0 and lse = -inf.  What lies in cells past kv_len, in
- * later tokens' or in other rows' cells never shows, NaN and infinities
+ * q and k enter as they are; scores, the softmax's maximum and sum and the sums of
+ * the product with v are fp32, and o is rounded once, to bf16.  That product's
+ * weights keep 15 bits where max_new * H_q / H_kv <= 16.  For longer chunks they are
+ * rounded to bf16 (2^-8 of themselves at most), the largest as well, because the
+ * maximum is raised only where it is passed by 2^8: o is off by 0.0023 of its norm,
+ * where its own rounding costs 0.0017.  A token that sees no position (kv_len < n_b,
+ * or a padding sequence on row 0) gets o = +0.0 and lse = -inf.  What lies in cells
+ * past kv_len, in later tokens' or in other rows' cells never shows, NaN and infinities
  * included.  A sequence with a row outside [0, R), kv_len outside
  * [0, table_width * page_size] or more than max_new tokens, and a token that
  * needs a page outside [1, N), gets NaN in o and lse.  A sequence whose token
