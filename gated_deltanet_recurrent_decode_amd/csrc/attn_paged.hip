@@ -17,10 +17,10 @@
 // the way.
 //
 // Work is dealt out by the key, not by the sequence: the units of 128 keys of all
-// (sequence, kv head, tile) triples lie on one line, cut into equal pieces, one a
-// workgroup.  A workgroup finds its piece from the lengths on the device (a
-// captured step follows its lengths) and finishes what lies whole in it; of a
-// triple that is cut it leaves (o, m, l) in the workspace for the second kernel.
+// (sequence, kv head) pairs, one tile each, lie on one line, cut into equal pieces,
+// one a workgroup.  A workgroup finds its piece from the lengths on the device (a
+// captured step follows its lengths) and finishes what lies whole in it; of a pair
+// that is cut it leaves (o, m, l) in the workspace for the second kernel.
 //
 // What bounds it: reading the cache.  MI355X: 64 sequences of 0.2-8 thousand tokens
 // at 16/4 heads of 256, 1.2 GB, 223 us a call (5.35 TB/s); 8 of 40-131 thousand e4m3
@@ -38,13 +38,13 @@ namespace gdn {
 
 namespace {
 
-constexpr int TM = 16;    // rows of a tile
+constexpr int TM = 16;    // rows of a tile, the most that a sequence has here
 constexpr int UNIT = 128; // keys of a unit: a block of 32 a wave
 constexpr int NT = 256;
 
-// A sequence's tiles of rows, and the units of each of them.
+// A sequence, and the units of each of its kv heads: one where it cannot be used.
 struct RowSeq : Seq {
-    int tiles, units;
+    int units;
 };
 
 __device__ __forceinline__ RowSeq read_row_seq(const AttnParams &p, int b)
@@ -52,14 +52,13 @@ __device__ __forceinline__ RowSeq read_row_seq(const AttnParams &p, int b)
     RowSeq s;
     static_cast<Seq &>(s) = read_seq(p, b);
     const int span = s.L - s.lo;
-    s.tiles = s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TM - 1) / TM);
-    s.units = span > UNIT ? (span + UNIT - 1) / UNIT : 1;
+    s.units = s.kind == kSkip ? 0 : (span > UNIT ? (span + UNIT - 1) / UNIT : 1);
     return s;
 }
 
 __device__ __forceinline__ long long seq_units(const AttnParams &p, const RowSeq &s)
 {
-    return (long long)p.H_kv * s.tiles * s.units;
+    return (long long)p.H_kv * s.units;
 }
 
 struct Place {
@@ -109,7 +108,6 @@ __device__ __forceinline__ Place locate(const AttnParams &p, Hit hit)
         f.s.L = __builtin_amdgcn_readlane(s.L, k);
         f.s.lo = __builtin_amdgcn_readlane(s.lo, k);
         f.s.r = __builtin_amdgcn_readlane(s.r, k);
-        f.s.tiles = __builtin_amdgcn_readlane(s.tiles, k);
         f.s.units = __builtin_amdgcn_readlane(s.units, k);
         return f;
     }
@@ -200,26 +198,37 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
             continue;
         }
         const long long v = u - before;
-        const long long ht = quotient(v, s.units);
-        const int unit0 = (int)(v - ht * s.units);
-        const int h = uniform((int)quotient(ht, s.tiles)), tile = uniform((int)(ht - (long long)h * s.tiles));
-        const long long t0 = before + ht * s.units, t1 = t0 + s.units;
+        const int h = uniform((int)quotient(v, s.units));
+        if (s.kind != kNormal) { // however many rows it has: zeros, or NaN
+            const uint32_t y = s.kind == kZero ? 0u : 0x7fc07fc0u;
+            for (int64_t x = tid; x < (int64_t)s.n * p.G * (D / 8); x += NT) {
+                const int64_t r = x / (D / 8), tk = s.first + r / p.G;
+                const int hq = h * p.G + (int)(r % p.G), c = (int)(x % (D / 8)) * 8;
+                *reinterpret_cast<u32x4 *>(p.out.p + tk * p.out.row + (int64_t)hq * p.out.head + c) =
+                    u32x4{y, y, y, y};
+                if (c == 0 && p.lse)
+                    p.lse[tk * p.H_q + hq] = s.kind == kZero ? neg_inf() : quiet_nan();
+            }
+            ++u;
+            continue;
+        }
+        const long long t0 = before + (long long)h * s.units, t1 = t0 + s.units;
+        const int unit0 = (int)(u - t0);
         const long long e = t1 < u_end ? t1 : u_end;
         const int unit1 = unit0 + (int)(e - u);
         const bool whole = u == t0 && e == t1;
         const int slot = u == u_begin ? 0 : 1;
         if (tid == 0 && u == t0 && e < t1)
-            write_cut(p, w, Cut{owner_of(at.total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, tile});
+            write_cut(p, w, Cut{owner_of(at.total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, 0});
         u = e;
 
         // this lane's row: a token and a head of the group
-        const int row = tile * TM + n_, rows = s.n * p.G;
-        const bool valid = row < rows && s.kind == kNormal;
-        const int tok = row / p.G, head = h * p.G + row % p.G;
+        const int rows = s.n * p.G;
+        const bool valid = n_ < rows;
+        const int tok = n_ / p.G, head = h * p.G + n_ % p.G;
         const int pos = valid ? s.L - s.n + tok : -1;
         const int low = p.window > 0 ? pos - p.window + 1 : 0;
-        const int last_row = (rows < (tile + 1) * TM ? rows : (tile + 1) * TM) - 1;
-        const int min_pos = s.L - s.n + tile * TM / p.G, max_pos = s.L - s.n + last_row / p.G;
+        const int min_pos = s.L - s.n; // the first token's
 
         bf16x8 qf[NS];
         const uint16_t *qp = p.q.p + (int64_t)(s.first + tok) * p.q.row + (int64_t)head * p.q.head;
@@ -253,8 +262,6 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
             // the next block's page numbers, while this one is worked on
             next[0] = page_of(key0 + UNIT);
             next[1] = page_of(key0 + UNIT + 16);
-            if (key0 > max_pos || (p.window > 0 && key0 + 31 <= min_pos - p.window))
-                continue; // no row of the tile sees the block
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (page[t] < 1 || page[t] >= p.N) { // uniform
@@ -325,7 +332,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
             settle(sc[1]);
 
             // masks, where some row of the tile does not see every key of the block
-            const bool mixed = key0 + 31 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
+            const bool mixed = key0 + 31 > min_pos || (p.window > 0 && key0 < s.L - p.window);
             float pr[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -437,12 +444,12 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
         }
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
-        // a needed page outside the pool, or a sequence that cannot be used
+        // a needed page outside the pool
         if (__shfl_xor((int)bad, 16) | (int)bad)
             bad = true;
         if (__shfl_xor((int)bad, 32) | (int)bad)
             bad = true;
-        if (bad || s.kind == kNan)
+        if (bad)
             l = quiet_nan();
 
         // the four waves' keys together
@@ -478,16 +485,15 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
         constexpr int C4 = D / 4;
         for (int x = tid; x < TM * C4; x += NT) {
             const int rr = x / C4, c = (x % C4) * 4;
-            const int ro = tile * TM + rr;
-            if (ro >= rows)
+            if (rr >= rows)
                 break;
             f32x4 o = *reinterpret_cast<const f32x4 *>(&sm_o[0][rr][c]);
 #pragma unroll
             for (int q = 1; q < 4; ++q)
                 o += *reinterpret_cast<const f32x4 *>(&sm_o[q][rr][c]);
             const float ll = sm_ll[rr];
-            const int64_t tk = s.first + ro / p.G;
-            const int hq = h * p.G + ro % p.G;
+            const int64_t tk = s.first + rr / p.G;
+            const int hq = h * p.G + rr % p.G;
             if (whole) {
                 const float vs = E4M3 ? p.v_scale[h] : 1.0f;
                 const float inv = ll == 0.f ? 0.f : vs / ll;
@@ -526,11 +532,10 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
     const bool alone = w1 - w0 < BATCH;
     const int rr = alone ? blockIdx.y * JW + wave : blockIdx.y;
     const int step = alone ? 1 : JW;
-    const int row = c.tile * TM + rr;
-    if (rr >= TM || row >= c.rows)
+    if (rr >= c.rows)
         return; // alone: each wave for itself, with no barrier behind
-    const int64_t t = c.first + row / p.G;
-    const int hq = h * p.G + row % p.G;
+    const int64_t t = c.first + rr / p.G;
+    const int hq = h * p.G + rr % p.G;
     float m = neg_inf(), l = 0.f, o[E];
 #pragma unroll
     for (int i = 0; i < E; ++i)
