@@ -6,8 +6,10 @@
 // eps); the pair (u, v) at angle a = position * freq becomes s (u cos a - v sin
 // a, v cos a + u sin a); the result is rounded once, to bf16 or to e4m3.
 //
-// The angle is formed in turns in fp64 and only its fraction goes on in fp32:
-// at position 2^20 an fp32 product would be off by 0.06 rad, this one by 1e-10.
+// The angle is formed in turns in fp64 and only its fraction, at most half a turn,
+// goes on in fp32: that rounding is off by 2^-26 of a turn at most, 1e-7 rad, at any
+// position (the fp64 part by 4e-10 rad at position 2^20, where an fp32 product would
+// be off by 0.06).
 //
 // A workgroup owns one token (and, when there are few tokens, one slice of its
 // heads): it forms the token's cos/sin table once in LDS, then every wave takes
@@ -231,8 +233,8 @@ static hipError_t launch_de(const AttnPrologueParams &p, hipStream_t stream)
     void *args[] = {&q};
     // Few tokens: past the heads that one pass takes, more workgroups a token, so that every load
     // leaves at once.  Many: one a token, which forms the angles once and loads three passes ahead
-    // (8570 tokens of 16 + 4 heads of 256: 48.5 us, 3.6 TB/s; a wave a token instead 50.5 us).  First
-    // way / second: 512 tokens of 16 + 4 heads of 256 12.0 / 11.4 us a call (the host's time), 1024
+    // (8570 tokens of 16 + 4 heads of 256: the kernel alone 48.2 us, a call 46.6 to 48.2, 3.7 TB/s, into an
+    // e4m3 cache 56.5; a wave a token instead 50.5 alone against 48.5).  First way / second: 512 tokens of 16 + 4 heads of 256 12.0 / 11.4 us a call (the host's time), 1024
     // tokens 11.9 / 12.1, 2048 tokens 17.2 / 13.8, 4096 tokens 28.9 / 22.6.
     const int per = 4 * 512 / D;
     if (p.T < 1024)
