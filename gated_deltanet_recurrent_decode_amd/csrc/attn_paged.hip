@@ -22,14 +22,16 @@
 // captured step follows its lengths) and finishes what lies whole in it; of a pair
 // that is cut it leaves (o, m, l) in the workspace for the second kernel.
 //
-// What bounds it: reading the cache.  MI355X: 64 sequences of 0.2-8 thousand tokens
-// at 16/4 heads of 256, 1.2 GB, 223 us a call (5.35 TB/s); 8 of 40-131 thousand e4m3
-// tokens at 32/4 heads of 128, 0.6 GB, 114 us (5.24 TB/s), 6 of them to join; one of 777
-// tokens 13 us, 11 + 4 alone, a chain of dependent reads (lengths, page numbers, keys).
-// What gave most after the layouts: page numbers read a block ahead by the scalar unit
-// (239 -> 228 us at the first size), the search within a wave (230 -> 225).  At 256
-// columns one workgroup a CU at a time with more registers is faster than two (230
-// against 235), at 128 two (110 -> 109).
+// What bounds it: reading the cache.  MI355X, calls back to back: 64 sequences of
+// 0.2-8 thousand tokens at 16/4 heads of 256, 1.2 GB, 224 us (5.34 TB/s); 8 of 40-131
+// thousand e4m3 tokens at 32/4 heads of 128, 0.6 GB, 115 us (5.17 TB/s), the join's
+// kernel 6.6 of them; one of 777 tokens 13.5 us, kernels of 10.4 and 4.1, a chain of
+// dependent reads (lengths, page numbers, keys).  What gave most after the layouts:
+// page numbers read a block ahead by the scalar unit (the kernel alone, under the
+// profiler, 239 -> 228 us at the first size), the search within a wave (11.6 -> 10.6
+// for the one sequence).  At 256 columns one workgroup a CU at a time with more
+// registers is faster than two (the first size 223 us a call, two 232), at 128 two are
+// no slower (long contexts 114.1, one 114.7).
 
 #include "attn_common.h"
 #include "gdn_internal.h"
@@ -614,8 +616,10 @@ __global__ __launch_bounds__(JT) void attn_join_kernel(AttnParams p)
 
 size_t attn_rows_layout(int d, void *base, AttnParams *p)
 {
-    // two a CU: 8 sequences of 40-131 thousand e4m3 tokens at 32/4 heads of 128 take 117 us, with
-    // one 156, with three 145; 32 sequences of 4 tokens over 0.05-3 thousand 30, 39 and 39
+    // Two a CU.  Us a call with one / two / three: 8 sequences of 40-131 thousand e4m3 tokens at 32/4
+    // heads of 128 129 / 114 / 122; 32 sequences of 4 tokens over 0.05-3 thousand at 32/8 heads of 128,
+    // window 1024, 38.7 / 34.4 / 36.6 (inputs that stay in the memory-side cache; 40 with others each
+    // call); 64 sequences of 0.2-8 thousand at 16/4 heads of 256 219 / 224 / 230.
     const int workgroups = 2 * device_cus();
     const size_t o = round256((size_t)workgroups * 2 * TM * d * 4), ml = round256((size_t)workgroups * 2 * TM * 2 * 4),
                  cut = round256((size_t)workgroups * 8 * 4);
@@ -653,10 +657,12 @@ hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t s
 }
 
 // Up to one tile of rows a sequence this kernel is used: it reads a sequence's keys once per 16
-// rows, the other (attn_tiles.hip) once for 256, but through LDS and with a third launch.  Rows
-// here / there in us, bf16: 64 sequences over 2-4 thousand tokens, 32/4 heads of 128: 8 rows 82 / 87,
-// 32 rows 135 / 95, 64 rows 247 / 105; 12 over 2-4 thousand, 16/2 heads of 256: 8 rows 35 / 38,
-// 32 rows 52 / 39; 8 over 0.5-1 thousand, 32/8 heads of 64: 16 rows 18 / 22, 32 rows 20 / 22.
+// rows, the other (attn_tiles.hip) once for 256, but through LDS and with a third launch, and its
+// weights are bf16.  Rows here / there in us a call, bf16: 64 sequences over 2-4 thousand tokens, 32/4
+// heads of 128: 8 rows 80 / 88, 16 rows 87 / 92; 8 over 0.5-1 thousand, 32/8 heads of 64: 4 rows 12.5 /
+// 21, 16 rows 16.6 / 21; 12 over 2-4 thousand, 16/2 heads of 256: 8 rows 33 / 37, 16 rows 41 / 36.5 (the
+// one point where there is faster).  With a tile per 16 rows this kernel lost past them: 32 rows 128 / 96
+// and 50 / 38 at the first and last of these, 64 rows 239 / 105.
 constexpr int kFewRows = 16;
 
 size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)

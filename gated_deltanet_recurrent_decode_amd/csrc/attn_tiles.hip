@@ -16,31 +16,35 @@
 //
 // The running maximum is only raised when a row's scores pass it by 2^8: weights
 // stay below 256, in fp32 and in bf16, and most blocks skip the rescaling of o
-// (raising it at once: 5 to 6% slower).  The largest weight of a row is then not 1
-// but rounded like the others, which shows in o as one more bf16 rounding of its
-// terms: 0.0023 of its norm from 64 bits in place of 0.0019.
+// (raising it at once: the two sizes below 4 and 9% slower).  The largest weight of a
+// row is then not 1 but rounded like the others, which shows in o as one more bf16
+// rounding of its terms: 0.0023 of its norm from 64 bits in place of 0.0019.
 //
 // Work is dealt out by the key: a first kernel lists every (sequence, kv head,
 // tile) with its blocks that the causal mask and the window leave; the line of
 // all blocks is cut into one piece a workgroup, and what is cut is joined by a
-// third kernel (26 us of 212 at 134 MB of parts, which lie in the workspace as they
-// lay in the registers: 1 KiB a store).
+// third kernel (26 us alone at 111 MB of parts, in the mixed step below; they lie in
+// the workspace as they lay in the registers: 1 KiB a store).
 //
 // What bounds it: the two waves of a SIMD get their products and their weights
 // overlapped by 40% only (counters: matrix cores busy 54% of the cycles, weights and
 // masks 48%, a quarter waiting), because a wave's own work is a chain: scores,
-// maximum, weights, products; and the card's power, for the clock falls to 1.7 GHz.  A
-// wave that forms its maximum goes before one with products, and that before one that
-// forms scores (s_setprio: 673 -> 663 us at the first size below).  Tried and slower, at
-// the same size when the kernel took 785 us under the profiler: the next block's scores
-// formed beside these weights (903; 32 more registers copied a block), the halves of the
-// workgroup one phase apart by two barriers a block (892) or by the place of a block's
-// one barrier (686 -> 704 us a call), the next block's loads spread between the score
-// products (844), two workgroups of 128 rows a CU (1% fewer cycles, but 663 -> 701 us a
-// call: k and v staged twice lower the clock), a step's first LDS reads before the step
-// (the same), 64 rows a wave and blocks of 64 keys at 256 columns (spills).  MI355X:
-// 4096 + 3001 tokens at 16/2 heads of 128 over 8-12 thousand others 663 us a call, 1006
-// TFLOP/s; a mixed step of 12 sequences at 16/2 heads of 256 212 us, 696 TFLOP/s.
+// maximum, weights, products; and the card's power, for the clock falls to 1.7 GHz.
+// MI355X, calls back to back, by card and session: 4096 + 3001 tokens at 16/2 heads of
+// 128 over 8-12 thousand others 653 to 700 us (1022 to 953 TFLOP/s; an e4m3 cache 683 to
+// 690, 64 columns 415 to 418, with a window of 1024 99 us and at 64 columns 68); a mixed
+// step of 12 sequences at 16/2 heads of 256 210 to 223 us (702 to 661 TFLOP/s; e4m3 220).
+//
+// A wave that forms its maximum goes before one with products, and that before one that
+// forms scores (s_setprio: the chunks 673 -> 663 us a call).  Tried and slower, calls on
+// one card each: the halves of the workgroup entering a block at different places (686 ->
+// 704 us), two workgroups of 128 rows a CU (1% fewer cycles, but 663 -> 701: k and v
+// staged twice lower the clock), weights as two bf16 numbers (699 -> 941, the mixed step
+// 222 -> 276).  The kernel alone under the profiler, from 785 us: the next block's scores
+// formed beside these weights (903; 32 more registers copied a block), the halves one
+// phase apart by two barriers a block (892), the next block's loads spread between the
+// score products (844).  A step's first LDS reads before the step: the same.  64 rows a
+// wave, and blocks of 64 keys at 256 columns: spills.
 
 #include "attn_common.h"
 #include "gdn_internal.h"
@@ -598,8 +602,8 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                             const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at], scale, off));
                             const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at + 1], scale, off));
                             l += e0 + e1;
-                            // rounded to bf16 for the matrix cores: off by at most 2^-9 of itself, and
-                            // o is rounded to bf16 in the end
+                            // rounded to bf16 for the matrix cores: off by at most 2^-8 of itself, as o is
+                            // in the end; two numbers for each take half of the products again (above)
                             pw[q & 1][i >> 1] = pack_bf16(e0, e1);
                         }
                     };
