@@ -44,7 +44,8 @@ constexpr int TM = 16;    // rows of a tile, the most that a sequence has here
 constexpr int UNIT = 128; // keys of a unit: a block of 32 a wave
 constexpr int NT = 256;
 
-// A sequence, and the units of each of its kv heads: one where it cannot be used.
+// A sequence, and the units of each of its kv heads: of keys, or where it cannot be used, and may
+// have any number of rows, of rows to fill.
 struct RowSeq : Seq {
     int units;
 };
@@ -53,7 +54,7 @@ __device__ __forceinline__ RowSeq read_row_seq(const AttnParams &p, int b)
 {
     RowSeq s;
     static_cast<Seq &>(s) = read_seq(p, b);
-    const int span = s.L - s.lo;
+    const int span = s.kind == kNormal ? s.L - s.lo : (s.kind == kSkip ? 0 : s.n * p.G);
     s.units = s.kind == kSkip ? 0 : (span > UNIT ? (span + UNIT - 1) / UNIT : 1);
     return s;
 }
@@ -201,11 +202,12 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_rows_kernel(AttnPar
         }
         const long long v = u - before;
         const int h = uniform((int)quotient(v, s.units));
-        if (s.kind != kNormal) { // however many rows it has: zeros, or NaN
+        if (s.kind != kNormal) { // zeros, or NaN
             const uint32_t y = s.kind == kZero ? 0u : 0x7fc07fc0u;
-            for (int64_t x = tid; x < (int64_t)s.n * p.G * (D / 8); x += NT) {
-                const int64_t r = x / (D / 8), tk = s.first + r / p.G;
-                const int hq = h * p.G + (int)(r % p.G), c = (int)(x % (D / 8)) * 8;
+            const int r0 = (int)(v - (long long)h * s.units) * UNIT, n = s.n * p.G - r0;
+            for (int x = tid; x < (n < UNIT ? n : UNIT) * (D / 8); x += NT) {
+                const int r = r0 + x / (D / 8), hq = h * p.G + r % p.G, c = x % (D / 8) * 8;
+                const int64_t tk = s.first + r / p.G;
                 *reinterpret_cast<u32x4 *>(p.out.p + tk * p.out.row + (int64_t)hq * p.out.head + c) =
                     u32x4{y, y, y, y};
                 if (c == 0 && p.lse)

@@ -234,8 +234,9 @@ static hipError_t launch_de(const AttnPrologueParams &p, hipStream_t stream)
     // Few tokens: past the heads that one pass takes, more workgroups a token, so that every load
     // leaves at once.  Many: one a token, which forms the angles once and loads three passes ahead
     // (8570 tokens of 16 + 4 heads of 256: the kernel alone 48.2 us, a call 46.6 to 48.2, 3.7 TB/s, into an
-    // e4m3 cache 56.5; a wave a token instead 50.5 alone against 48.5).  First way / second: 512 tokens of 16 + 4 heads of 256 12.0 / 11.4 us a call (the host's time), 1024
-    // tokens 11.9 / 12.1, 2048 tokens 17.2 / 13.8, 4096 tokens 28.9 / 22.6.
+    // e4m3 cache 56.5; a wave a token instead 50.5 alone against 48.5).  First way / second: 512 tokens of
+    // 16 + 4 heads of 256 12.0 / 11.4 us a call (the host's time), 1024 tokens 11.9 / 12.1, 2048 tokens
+    // 17.2 / 13.8, 4096 tokens 28.9 / 22.6.
     const int per = 4 * 512 / D;
     if (p.T < 1024)
         return hipLaunchKernel(reinterpret_cast<const void *>(&attn_prologue_kernel<D, E4M3, 1>),

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from tests import attn_helpers as A
+from tests import attn_norms as N
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,35 @@ def test_overlapping_ranges_of_more_tiles_than_32_bits_count(gdn):
     torch.cuda.synchronize()
     assert (big[:4096] == 0x5A).all() and (big[4096 + need:] == 0x5A).all()
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("B", [6, 90])
+def test_unusable_sequences_of_many_rows_among_single_tokens(gdn, d, kind, B):
+    """Sequences longer than max_new (NaN) and padding sequences of any length (zeros), in the kernel of few rows:
+    one row more and less than the 128 that a workgroup fills at a time, and many times that."""
+    long = [31, 32, 33, 64, 65, 1100]
+    lens = [(long[i % 6], 5) if i % 2 else (1, 40 + (97 * i) % 1500) for i in range(B)]
+    c = A.Cache(lens, H_q=8, H_kv=2, d=d, page=16, kind=kind, seed=37)
+    row = c.row.clone()
+    row[1::4] = 0
+    q = torch.cat([c.q.cuda(), torch.zeros(3, 8, d, dtype=A.BF, device="cuda")])
+    out, lse = torch.full_like(q, 7.0), torch.full((c.T + 3, 8), 7.0, device="cuda")
+    a = c.cuda(row=row)
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(B, c.T + 3, 1, 8, 2, d), dtype=torch.uint8, device="cuda")
+    gdn.attn_paged(q, a["k_pages"], a["v_pages"], a["page_table"], a["kv_len"], a["row"], a["cu_seqlens"], out, ws,
+                   max_new=1, lse=lse, k_scale=a["k_scale"], v_scale=a["v_scale"])
+    torch.cuda.synchronize()
+    want, want_lse, tol, tol_l = N.attention(c, d ** -0.5, 0, "cuda")
+    out, lse = out.cpu(), lse.cpu()
+    for b in range(B):
+        t = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        if row[b] == 0:
+            assert (out[t] == 0).all() and (lse[t] == -torch.inf).all(), b
+        elif b % 2:
+            assert out[t].isnan().all() and lse[t].isnan().all(), b
+        else:
+            N.check_norms(out[t], want[t], tol[t], f"sequence {b}")
+            A.check(lse[t], want_lse[t], tol_l[t], f"sequence {b}")
+    assert (out[c.T:] == 7).all() and (lse[c.T:] == 7).all()
