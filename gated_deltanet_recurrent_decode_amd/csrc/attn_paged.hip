@@ -23,9 +23,9 @@
 // that is cut it leaves (o, m, l) in the workspace for the second kernel.
 //
 // What bounds it: reading the cache.  MI355X, calls back to back: 64 sequences of
-// 0.2-8 thousand tokens at 16/4 heads of 256, 1.2 GB, 224 us (5.34 TB/s); 8 of 40-131
-// thousand e4m3 tokens at 32/4 heads of 128, 0.6 GB, 115 us (5.17 TB/s), the join's
-// kernel 6.6 of them; one of 777 tokens 13.5 us, kernels of 10.4 and 4.1, a chain of
+// 0.2-8 thousand tokens at 16/4 heads of 256, 1.2 GB, 223 us (5.36 TB/s); 8 of 40-131
+// thousand e4m3 tokens at 32/4 heads of 128, 0.6 GB, 113 us (5.25 TB/s), the join's
+// kernel 6.3 of them; one of 777 tokens 13.0 us, kernels of 9.4 and 4.2, a chain of
 // dependent reads (lengths, page numbers, keys).  What gave most after the layouts:
 // page numbers read a block ahead by the scalar unit (the kernel alone, under the
 // profiler, 239 -> 228 us at the first size), the search within a wave (11.6 -> 10.6

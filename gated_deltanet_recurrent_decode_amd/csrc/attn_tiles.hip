@@ -32,8 +32,9 @@
 // maximum, weights, products; and the card's power, for the clock falls to 1.7 GHz.
 // MI355X, calls back to back, by card and session: 4096 + 3001 tokens at 16/2 heads of
 // 128 over 8-12 thousand others 653 to 700 us (1022 to 953 TFLOP/s; an e4m3 cache 683 to
-// 690, 64 columns 415 to 418, with a window of 1024 99 us and at 64 columns 68); a mixed
-// step of 12 sequences at 16/2 heads of 256 210 to 223 us (702 to 661 TFLOP/s; e4m3 220).
+// 690, 64 columns 415 to 423, with a window of 1024 99 to 102 and at 64 columns 68 to 71);
+// a mixed step of 12 sequences at 16/2 heads of 256 210 to 223 us (702 to 661 TFLOP/s;
+// e4m3 220 to 225).
 //
 // A wave that forms its maximum goes before one with products, and that before one that
 // forms scores (s_setprio: the chunks 673 -> 663 us a call).  Tried and slower, calls on
