@@ -19,7 +19,8 @@ __all__ = ["GdnError", "lib", "gdn_decode_step", "gdn_decode_step_commit", "gdn_
            "slot_commit",
            "slot_reset", "slot_copy", "check_slots", "traffic_probe", "status_string", "LIB_PATH", "EXPORTS",
            "rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "kv_page_workspace_bytes",
-           "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact"]
+           "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact",
+           "lin_attn_step", "lin_attn_step_tokens", "lin_attn_prefill", "lin_attn_prefill_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -107,6 +108,7 @@ def lib() -> ctypes.CDLL:
     L.gdn_traffic_probe.restype = i32
     L.gdn_traffic_probe.argtypes = [ctypes.POINTER(Probe), i32, i32, i32, i32, i32, P, P, P, P, P]
     _attention.declare(L)
+    _linear.declare(L)
     _lib = L
     return L
 
@@ -549,3 +551,11 @@ from .attention import (attn_paged, attn_paged_workspace_bytes, attn_prologue, k
                         rope_freqs)
 
 EXPORTS += _attention.EXPORTS
+
+# ------------------------------------------------------------------ linear attention with a decay for each head
+
+from . import linear as _linear  # noqa: E402
+from .linear import (lin_attn_prefill, lin_attn_prefill_workspace_bytes, lin_attn_step,  # noqa: E402
+                     lin_attn_step_tokens)
+
+EXPORTS += _linear.EXPORTS

@@ -591,6 +591,90 @@ gdn_status kv_page_copy(const gdn_pages *pages, const int32_t *src, const int32_
 gdn_status kv_page_compact(const gdn_pages *pages, int32_t *remap, int32_t *result, void *workspace,
                            size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head, the layers of other hybrid models
+ * that keep a state of the same form in the same kind of slots, without the conv
+ * and the delta rule.
+ *
+ * gdn_lin_dims (GDN_ERR_SHAPE past these: B*H_v below 2^20, T and B*T below 2^30)
+ *   B  rows, or sequences;  T  tokens a row, or of all sequences together;  H_k
+ *   query and key heads;  H_v  value heads, a multiple of H_k: value head hv
+ *   reads q and k of head hv / (H_v / H_k);  d_k, d_v  64 or 128;  N  slots with
+ *   the null slot 0;  per_token  g holds 0: a log decay for each head [H_v], 1: one
+ *   for each token and head too
+ * q, k, v and out by gdn_heads (row strides up to 2^24); out overlaps none of
+ * them.  state [N][H_v][d_k][d_v] fp32, S[i][j] with i over keys, 16-byte aligned.
+ * Log decays below -177 count as -177 (e^-177 is 0 in fp32). */
+typedef struct gdn_lin_dims {
+    int32_t B, T, H_k, H_v, d_k, d_v, N, per_token;
+} gdn_lin_dims;
+
+/*
+ * lin_attn_step -- single decoding tokens, or T a row, in order: for each row r
+ * with rs = read_slot[r] and ws = write_slot[r] (rs where write_slot is NULL), S
+ * from slot rs, for each token and value head hv in fp32
+ *   S <- e^g S + k v^T;  o = q_scale S^T q, rounded once, to bf16
+ * and at the end S goes to slot ws.  Token t of row r is token r*T + t of q, k, v
+ * and out; g [H_v] or [B][T][H_v].  Twin writes may have T > 1 here: the whole state
+ * of a row is held until its end.
+ * A row with rs == 0 is padding: out +0.0, no slot touched.  A row with a slot
+ * outside [0, N), and a real row of a twin write whose write slot is 0 or its read
+ * slot, gets NaN in out and touches no slot.  Preconditions, not checked: no two
+ * rows write one slot, and none writes another's read slot.
+ * B = 0 returns GDN_OK at once.  GDN_ERR_NULL, GDN_ERR_SHAPE (sizes, q_scale not
+ * finite), GDN_ERR_UNSUPPORTED (head dims, alignment).
+ */
+gdn_status lin_attn_step(const gdn_lin_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
+                         const float *g, float *state, const int32_t *read_slot, const int32_t *write_slot,
+                         const gdn_heads *out, float q_scale, hipStream_t stream);
+
+/*
+ * lin_attn_step_tokens -- lin_attn_step over T tokens a row that keeps the state
+ * after token t in slot token_slots[r*T + t] where that is not 0, for the verify pass
+ * of speculative decoding; slot rs is not written.  A row with a slot outside [0, N)
+ * or a token slot equal to its read slot gets NaN in out and touches no slot.
+ * Preconditions, not checked: the token slots that are not 0 are distinct and no
+ * row's read slot.
+ */
+gdn_status lin_attn_step_tokens(const gdn_lin_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
+                                const float *g, float *state, const int32_t *read_slot, const int32_t *token_slots,
+                                const gdn_heads *out, float q_scale, hipStream_t stream);
+
+/*
+ * lin_attn_prefill -- the same recurrence over packed prompts, in chunks: sequence b
+ * owns tokens cu_seqlens[b] .. cu_seqlens[b+1]-1, begins with the state of read_slot[b]
+ * (with zeros where that is 0 and write_slot[b] is not) and leaves its state in
+ * write_slot[b] (read_slot[b] where write_slot is NULL).  Several sequences may begin
+ * with the same slot if none writes it.  A sequence without tokens moves its state.
+ * g [H_v] or [T][H_v].
+ * Sums, states and decays are fp32 (a chunk's sums of log decays 64 bits).  For the
+ * matrix cores, decayed values go into the state as three bf16 numbers, with all their
+ * bits; the state and the weights that make a read-out go as two, off by at most
+ * 2^-15 of themselves, before o is rounded once, to bf16.
+ * Results match lin_attn_step within rounding, not bit for bit, and the same call gives
+ * the same bits again.  An infinity or NaN in a token shows from that token on, as an
+ * infinity or NaN, and nowhere before.
+ * A sequence with both slots 0 is padding: out +0.0, no slot touched.  One with a
+ * slot outside [0, N), or that reads a slot and writes slot 0, gets NaN in out and
+ * touches no slot.  One whose token range is not inside [0, T] is left as it was, and
+ * so are tokens outside [cu_seqlens[0], cu_seqlens[B]).  Preconditions, not checked:
+ * cu_seqlens is non-decreasing; no two sequences write one slot, and none writes
+ * another's read slot.
+ * workspace: lin_attn_prefill_workspace_bytes(dims) bytes of device memory, 256-byte
+ * aligned, contents of no matter before and after; calls that share one must be
+ * stream-ordered.
+ * B = 0 returns GDN_OK at once; with T = 0 the arrays of tokens may be NULL.  Statuses
+ * as lin_attn_step; GDN_ERR_SHAPE also for a workspace too small.
+ */
+gdn_status lin_attn_prefill(const gdn_lin_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
+                            const float *g, const int32_t *cu_seqlens, float *state, const int32_t *read_slot,
+                            const int32_t *write_slot, const gdn_heads *out, float q_scale, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* The workspace lin_attn_prefill needs for dims (B, T, H_v, d_k, d_v); 0 when dims is
+ * NULL or its sizes are unusable. */
+size_t lin_attn_prefill_workspace_bytes(const gdn_lin_dims *dims);
+
 /* Static text for a status code (host only). */
 const char *gdn_status_string(gdn_status status);
 
