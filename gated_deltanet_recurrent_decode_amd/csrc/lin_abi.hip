@@ -26,8 +26,8 @@ gdn_status check_dims(const gdn_lin_dims &d)
 
 gdn_status check_heads(const gdn_heads &h)
 {
-    // a chunk's rows are addressed in 32 bits
-    if (h.row_stride < 0 || h.head_stride < 0 || h.row_stride > 1 << 24)
+    // a chunk's rows, and a few heads of them, are addressed in 32 bits
+    if (h.row_stride < 0 || h.head_stride < 0 || h.row_stride > 1 << 24 || h.head_stride > 1 << 24)
         return GDN_ERR_SHAPE;
     return !aligned(h.data, 16) || h.row_stride % 8 != 0 || h.head_stride % 8 != 0 ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }

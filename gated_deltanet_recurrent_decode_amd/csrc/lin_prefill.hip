@@ -29,8 +29,15 @@ namespace gdn {
 namespace {
 
 constexpr int C = 32; // tokens of a chunk
+#ifndef LIN_WAVES
+#define LIN_WAVES 2
+#endif
+#ifndef LIN_TARGET
+#define LIN_TARGET 8
+#endif
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
@@ -44,6 +51,42 @@ __device__ __forceinline__ float log2_decay(float g)
     return x < kLeast ? kLeast : x; // a NaN stays
 }
 
+// The logarithm range that a state and a chunk's weights may share one scale in: 2^-64 .. 2^64.
+constexpr float kRange = 64.0f;
+
+// 2^x of a 64-bit logarithm: its fraction keeps all bits of fp32.
+__device__ __forceinline__ float exp2_of(double x)
+{
+    const double n = __builtin_rint(x);
+    return ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v)
+{
+    const uint64_t x = __builtin_bit_cast(uint64_t, v);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+
+// Inclusive sums over each half of the wave, by moves within rows of 16 and one of a row's last value.
+__device__ __forceinline__ double scan32(double v)
+{
+    v += dpp_or_zero<0x111, 0xF>(v);
+    v += dpp_or_zero<0x112, 0xF>(v);
+    v += dpp_or_zero<0x114, 0xF>(v);
+    v += dpp_or_zero<0x118, 0xF>(v);
+    return v + dpp_or_zero<0x142, 0xA>(v);
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    const uint64_t x = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)x, lane), hi = __builtin_amdgcn_readlane((int)(x >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // 16 bytes a lane from base + off into LDS, lane after lane from `to` on.  As inline assembly because
 // the compiler, given the builtin, waits for it before any read of LDS.  Whoever reads `to` waits for
 // vmcnt(0) and a barrier first.
@@ -53,6 +96,14 @@ __device__ __forceinline__ void load_to_lds(lds_byte *to, const uint8_t *base, i
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)at)), "v"(off),
                  "s"(base)
                  : "memory"); // m0 is reserved: whatever of the compiler's own needs it sets it first
+}
+
+// The same of 4 bytes a lane.
+__device__ __forceinline__ void load_dword_to_lds(lds_byte *to, const float *at)
+{
+    const uint32_t m = (uint32_t)(uintptr_t)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)m)), "v"(at)
+                 : "memory");
 }
 
 // A segment of a sequence.  Segment s of sequence b has place cu[b] / segment + b + s: no two the same, and
@@ -141,42 +192,53 @@ __device__ __forceinline__ bf16x8 operand(const uint32_t (&x)[4])
     return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], x[2], x[3]});
 }
 
-__device__ __forceinline__ bool not_finite(uint32_t pair)
-{
-    return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
-}
-
 } // namespace
 
+// A workgroup takes HPW value heads of one key head, a wave 32 columns of one of them.
 // OUT: the walk, with read-outs.  Otherwise a segment's own part of the state, for all but a
 // sequence's last.
-template <int DK, int DV, bool OUT>
-__global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams p)
+//
+// What the waves of a head would all compute is dealt out among them a chunk ahead and goes through LDS: the
+// weighted scores w_ij = q_scale (q_i . k_j) 2^(G_i - G_j), as pairs of bf16 numbers, and the scales of the
+// tokens.  So there is one barrier a chunk.
+template <int DK, int DV, int HPW, bool OUT>
+__global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(LinPrefillParams p)
 {
-    constexpr int NW = DV / 32, NT = 64 * NW;
-    constexpr int TK = DK / 32;             // 32-row tiles of S
-    constexpr int KB = C * DK * 2, VB = C * DV * 2; // bytes of a chunk's k (and q), v
-    constexpr int BUF = (OUT ? 2 : 1) * KB + VB;
-    __shared__ __align__(16) uint8_t sm[2][BUF];
-    __shared__ __align__(16) float sm_hi[NW][C], sm_lo[NW][C];
+    constexpr int WPH = DV / 32, NW = WPH * HPW, NT = 64 * NW;
+    constexpr int TK = DK / 32;                     // 32-row tiles of S
+    constexpr int KB = C * DK * 2, VB = C * DV * 2; // bytes of a chunk's k (and q), of a head's v
+    constexpr int QKB = (OUT ? 2 : 1) * KB;
+    constexpr int IK = KB / (1024 * NW), IV = HPW * VB / (1024 * NW); // instructions a wave that bring them
+    constexpr int PR = 80; // bytes of a row of scores: 64, and room against bank conflicts
+    __shared__ __align__(16) uint8_t sm_qk[3][QKB], sm_v[2][HPW * VB];
+    __shared__ __align__(16) float sm_g[3][HPW][64];
+    __shared__ __align__(16) uint8_t sm_p[OUT ? 2 : 1][HPW][2][OUT ? C * PR : 16];
+    __shared__ __align__(16) float sm_G[OUT ? NW : 1][2][C]; // a wave's own: sums of log decays
+    __shared__ __align__(16) float sm_begin[2][HPW][C], sm_b[2][HPW][C];
+    __shared__ float sm_f[2][HPW];
+    __shared__ double sm_off[2][HPW], sm_total[2][HPW];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
     // consecutive items (heads fastest) on one XCD: heads that share q and k meet in its L2
-    const int items = p.segments * p.H_v, per = (items + 7) >> 3;
+    const int groups = p.H_v / HPW, items = p.segments * groups, per = (items + 7) >> 3;
     const int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (item >= items || (int)(blockIdx.x >> 3) >= per)
         return;
-    const int place = item / p.H_v, hv = item % p.H_v, hk = hv / (p.H_v / p.H_k);
+    const int place = item / groups, h0 = item % groups * HPW, hk = h0 / (p.H_v / p.H_k);
+    const int hw = wave / WPH, hv = h0 + hw, col0 = wave % WPH * 32;
     const Segment sg = segment_at(p, place);
     if (sg.b < 0)
         return;
     if (sg.pad || sg.bad) {
         if constexpr (OUT) {
             const uint32_t y = sg.pad ? 0u : 0x7fc07fc0u;
-            for (int x = tid; x < sg.n * (DV / 8); x += NT)
-                *reinterpret_cast<u32x4 *>(p.out.p + (int64_t)(sg.first + x / (DV / 8)) * p.out.row +
-                                           (int64_t)hv * p.out.head + x % (DV / 8) * 8) = u32x4{y, y, y, y};
+            constexpr int CH = HPW * DV / 8;
+            for (int x = tid; x < sg.n * CH; x += NT) {
+                const int h = h0 + x % CH / (DV / 8), c = x % (DV / 8) * 8;
+                *reinterpret_cast<u32x4 *>(p.out.p + (int64_t)(sg.first + x / CH) * p.out.row +
+                                           (int64_t)h * p.out.head + c) = u32x4{y, y, y, y};
+            }
         }
         return;
     }
@@ -185,9 +247,9 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
         return;
 
     // this lane's column of v, and the rows of S
-    const int col = wave * 32 + swapped(n_);
     const int64_t tile = (int64_t)DK * DV;
-    auto row_of = [&](int t, int i) { return 32 * t + 16 * (i >> 3) + 8 * hh + (i & 7); };
+    const int cell = 8 * hh * DV + col0 + swapped(n_);
+    auto cell_of = [&](int t, int i) { return cell + (32 * t + 16 * (i >> 3) + (i & 7)) * DV; };
     f32x16 S[TK];
     const float *from = nullptr;
     if (OUT && sg.count > 1)
@@ -199,7 +261,7 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
         for (int t = 0; t < TK; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                S[t][i] = from[row_of(t, i) * DV + col];
+                S[t][i] = from[cell_of(t, i)];
     } else {
 #pragma unroll
         for (int t = 0; t < TK; ++t)
@@ -207,44 +269,82 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
             for (int i = 0; i < 16; ++i)
                 S[t][i] = 0.f;
     }
-    auto store_state = [&](float *to) {
+    auto store_state = [&](float *to) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < TK; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                to[row_of(t, i) * DV + col] = S[t][i];
+                to[cell_of(t, i)] = S[t][i];
     };
+
     if (!OUT && sg.s == 0) // the walk may find the slot already written: it begins from this copy
         store_state(p.entry + ((int64_t)place * p.H_v + hv) * tile);
 
     // staging: 1 KiB an instruction, whole rows, chunks of 16 bytes in the order of their row
-    auto stage = [&](auto width, const Heads &x, int head, lds_byte *to, int c0) {
-        constexpr int D = decltype(width)::value, CH = D / 8, RP = 64 / CH;
-        const int rows = sg.n - c0 < C ? sg.n - c0 : C;
-        const uint64_t from =
-            reinterpret_cast<uint64_t>(x.p + (int64_t)(sg.first + c0) * x.row + (int64_t)head * x.head);
-        const uint8_t *base = reinterpret_cast<const uint8_t *>(
-            (uint64_t)(uint32_t)uniform((int)(from >> 32)) << 32 | (uint32_t)uniform((int)from));
-#pragma unroll
-        for (int i = 0; i < C / RP / NW; ++i) {
-            const int r0 = (i * NW + wave) * RP, r = r0 + lane / CH;
-            const int rr = r < rows ? r : rows - 1; // rows past the last repeat it
-            load_to_lds(to + r0 * D * 2, base, rr * (int)x.row * 2 + ((lane % CH) ^ swizzle<D>(r)) * 16);
-        }
+    auto offset = [&](auto width, const Heads &x, int i, int last) { // this lane's; rows past the last repeat it
+        constexpr int D = decltype(width)::value, CH = D / 8, RP = 64 / CH, PER = C / RP; // instructions a head
+        const int at = i * NW + wave, r = at % PER * RP + lane / CH;
+        return (r < last ? r : last) * (int)x.row * 2 + at / PER * (int)x.head * 2 +
+               ((lane % CH) ^ swizzle<D>(r)) * 16;
     };
     const std::integral_constant<int, DK> width_k;
     const std::integral_constant<int, DV> width_v;
-    auto bring = [&](int buf, int c0) {
-        lds_byte *to = (lds_byte *)sm + buf * BUF;
-        stage(width_k, p.k, hk, to, c0);
-        stage(width_v, p.v, hv, to + KB, c0);
-        if constexpr (OUT)
-            stage(width_k, p.q, hk, to + KB + VB, c0);
+    int off_k[IK], off_v[IV], off_q[IK];
+#pragma unroll
+    for (int i = 0; i < IK; ++i) {
+        off_k[i] = offset(width_k, p.k, i, C - 1);
+        off_q[i] = offset(width_k, p.q, i, C - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < IV; ++i)
+        off_v[i] = offset(width_v, p.v, i, C - 1);
+    auto base_of = [&](const Heads &x, int head, int token) { // in scalar registers
+        const uint64_t at =
+            reinterpret_cast<uint64_t>(x.p + (int64_t)(sg.first + token) * x.row + (int64_t)head * x.head);
+        return reinterpret_cast<const uint8_t *>((uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32 |
+                                                 (uint32_t)uniform((int)at));
     };
-    // a token's log decay, of this lane's token of a chunk
-    auto decay_of = [&](int c0) {
-        const int t = c0 + n_;
-        return t < sg.n ? p.g[p.per_token ? (int64_t)(sg.first + t) * p.H_v + hv : hv] : 0.f;
+    int coming = 0, coming_v = 0; // tokens whose q and k, and whose v, were asked for
+    auto bring_qk = [&](int buf) {
+        lds_byte *to = (lds_byte *)sm_qk + buf * QKB + wave * 1024;
+        const int last = sg.n - coming - 1;
+        if (last < C - 1) {
+#pragma unroll
+            for (int i = 0; i < IK; ++i) {
+                off_k[i] = offset(width_k, p.k, i, last);
+                off_q[i] = offset(width_k, p.q, i, last);
+            }
+        }
+        const uint8_t *base_k = base_of(p.k, hk, coming);
+#pragma unroll
+        for (int i = 0; i < IK; ++i)
+            load_to_lds(to + i * NW * 1024, base_k, off_k[i]);
+        if constexpr (OUT) {
+            const uint8_t *base_q = base_of(p.q, hk, coming);
+#pragma unroll
+            for (int i = 0; i < IK; ++i)
+                load_to_lds(to + KB + i * NW * 1024, base_q, off_q[i]);
+        }
+        if (wave < HPW) { // the decays, a wave a head
+            const int t = coming + (n_ < last ? n_ : last), h = h0 + wave;
+            load_dword_to_lds((lds_byte *)sm_g + (buf * HPW + wave) * 256,
+                              p.g + (p.per_token ? (int64_t)(sg.first + t) * p.H_v + h : (int64_t)h));
+        }
+        coming += C;
+    };
+    auto bring_v = [&](int buf) {
+        lds_byte *to = (lds_byte *)sm_v + buf * (HPW * VB) + wave * 1024;
+        const int last = sg.n - coming_v - 1;
+        if (last < C - 1) {
+#pragma unroll
+            for (int i = 0; i < IV; ++i)
+                off_v[i] = offset(width_v, p.v, i, last);
+        }
+        const uint8_t *base_v = base_of(p.v, h0, coming_v);
+#pragma unroll
+        for (int i = 0; i < IV; ++i)
+            load_to_lds(to + i * NW * 1024, base_v, off_v[i]);
+        coming_v += C;
     };
 
     // transposing reads: lane (hv, r, c) points at key 4 hv + r (+ 8 for the second), columns 4 c
@@ -254,8 +354,10 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
     for (int y = 0; y < 2; ++y) {
         const int key = 8 * y + 4 * (gr >> 1) + r_, chunk = (gr & 1) * 2 + (c_ >> 1);
         tk_at[y] = key * DK * 2 + ((chunk ^ swizzle<DK>(key)) * 16) + (c_ & 1) * 8;
-        tv_at[y] = key * DV * 2 + (((wave * 4 + chunk) ^ swizzle<DV>(key)) * 16) + (c_ & 1) * 8;
+        tv_at[y] = hw * VB + key * DV * 2 + (((col0 / 8 + chunk) ^ swizzle<DV>(key)) * 16) + (c_ & 1) * 8;
     }
+    // row reads: this lane's row, its chunk without the step's
+    const int row_at = n_ * DK * 2 + (hh ^ swizzle<DK>(n_)) * 16;
     auto transposed = [&](const uint8_t *at0, const uint8_t *at1, uint32_t (&x)[4]) {
         const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at0));
         const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at1));
@@ -265,92 +367,155 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
         x[3] = b[1];
     };
 
-    float total = 1.f; // what the segment leaves of the state that it begins with
-    float g_next = decay_of(0);
-    if (sg.n > 0)
-        bring(0, 0);
-    for (int c0 = 0, buf = 0; c0 < sg.n; c0 += C, buf ^= 1) {
-        const float g = g_next;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // this wave's part of the chunk is in LDS
-        __syncthreads();
-        if (c0 + C < sg.n) {
-            g_next = decay_of(c0 + C);
-            bring(buf ^ 1, c0 + C);
-        }
+    // The state is held without its latest decays, S = 2^off S~: with L_i = off + G_i, o_i = 2^(L_i) S~^T q_i
+    // + sum_j w_ij v_j and S~ += k_j (2^(-L_j) v_j)^T, with no decay of the whole state, until some |L_i| of
+    // a chunk passes kRange.  There S~ takes the scale of the chunk's end, 2^(off + G_end), and off is -G_end
+    // for its weights.
+    auto sums = [&](int c0, int buf, int head) { // G of this lane's token
         const int rows = sg.n - c0 < C ? sg.n - c0 : C;
-        const uint8_t *kb = sm[buf], *vb = kb + KB, *qb = vb + VB;
-
-        // G_n of this lane's token, in 64 bits, as two fp32 numbers: differences of large sums keep their bits
-        double G = n_ < rows ? (double)log2_decay(g) : 0.0;
-#pragma unroll
-        for (int m = 1; m < C; m <<= 1) {
-            const double o = __shfl_up(G, m, 32);
-            if (n_ >= m)
-                G += o;
+        return scan32(n_ < rows ? (double)log2_decay(sm_g[buf][head][n_]) : 0.0);
+    };
+    auto scales = [&](int c0, int c, int buf, int head) { // of chunk c, at token c0
+        const double G = sums(c0, buf, head), end = lane_value(G, C - 1);
+        const double off = c > 0 ? sm_off[(c - 1) & 1][head] : 0.0, total = c > 0 ? sm_total[(c - 1) & 1][head] : 0.0;
+        const bool far = __ballot(fabs(off + G) > (double)kRange) != 0;
+        const double base = far ? -end : off;
+        if (hh == 0) {
+            sm_begin[c & 1][head][n_] = exp2_of(off + G) * p.q_scale;
+            sm_b[c & 1][head][n_] = c0 + n_ < sg.n ? exp2_of(-(base + G)) : 0.f;
         }
+        if (lane == 0) {
+            sm_f[c & 1][head] = far ? exp2_of(off + end) : 1.f;
+            sm_off[c & 1][head] = base + end;
+            sm_total[c & 1][head] = total + end;
+        }
+    };
+    // the scores of keys 16 kt.. and tokens 16 tt.., 16 x 16 x 32 products: a lane has a token and four keys
+    auto scores = [&](int c0, int c, int buf, int head, int kt, int tt) {
+        const double G = sums(c0, buf, head);
         const float G_hi = (float)G, G_lo = (float)(G - (double)G_hi);
         if (hh == 0) {
-            sm_hi[wave][n_] = G_hi;
-            sm_lo[wave][n_] = G_lo;
+            sm_G[wave][0][n_] = G_hi;
+            sm_G[wave][1][n_] = G_lo;
         }
-        const float E_hi = __shfl(G_hi, 31), E_lo = __shfl(G_lo, 31);
-        const float keep = __builtin_amdgcn_exp2f(E_hi + E_lo);
-        total *= keep;
+        const int m = lane & 15, g4 = lane >> 4;
+        const uint8_t *kb = sm_qk[buf], *qb = kb + KB;
+        f32x4 P = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < DK / 32; ++x) {
+            const int at = ((4 * x + g4) ^ swizzle<DK>(m)) * 16;
+            const u32x4 kf = *reinterpret_cast<const u32x4 *>(kb + (16 * kt + m) * DK * 2 + at);
+            const u32x4 qf = *reinterpret_cast<const u32x4 *>(qb + (16 * tt + m) * DK * 2 + at);
+            P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), __builtin_bit_cast(bf16x8, qf),
+                                                        P, 0, 0, 0);
+        }
+        settle(P);
         __builtin_amdgcn_wave_barrier();
-        f32x4 K_hi[4], K_lo[4]; // of the keys of this lane's rows
+        const float T_hi = sm_G[wave][0][16 * tt + m], T_lo = sm_G[wave][1][16 * tt + m];
+        const f32x4 K_hi = *reinterpret_cast<const f32x4 *>(&sm_G[wave][0][16 * kt + 4 * g4]);
+        const f32x4 K_lo = *reinterpret_cast<const f32x4 *>(&sm_G[wave][1][16 * kt + 4 * g4]);
+        float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            K_hi[i] = *reinterpret_cast<const f32x4 *>(&sm_hi[wave][8 * i + 4 * hh]);
-            K_lo[i] = *reinterpret_cast<const f32x4 *>(&sm_lo[wave][8 * i + 4 * hh]);
+            const float d = (T_hi - K_hi[i]) + (T_lo - K_lo[i]);
+            w[i] = kt < tt || 4 * g4 + i <= m ? P[i] * p.q_scale * __builtin_amdgcn_exp2f(d) : 0.f;
         }
+        u32x2 hi, lo;
+        uint32_t x, y;
+        split2(w[0], w[1], x, y);
+        hi[0] = x, lo[0] = y;
+        split2(w[2], w[3], x, y);
+        hi[1] = x, lo[1] = y;
+        // keys in the order of the product with v: blocks of four, 0 2 1 3
+        const int at = (16 * tt + m) * PR + kt * 32 + ((g4 & 1) * 2 + (g4 >> 1)) * 8;
+        *reinterpret_cast<u32x2 *>(&sm_p[c & 1][head][0][at]) = hi;
+        *reinterpret_cast<u32x2 *>(&sm_p[c & 1][head][1][at]) = lo;
+        __builtin_amdgcn_wave_barrier();
+    };
+    auto ahead = [&](int c0, int c, int buf) {
+        constexpr int JOBS = OUT ? 4 : 1; // a head
+        for (int job = wave; job < JOBS * HPW; job += NW) {
+            const int head = job / JOBS, x = job % JOBS;
+            if (x == JOBS - 1)
+                scales(c0, c, buf, head);
+            else if constexpr (OUT)
+                scores(c0, c, buf, head, x == 2, x > 0);
+        }
+    };
 
-        uint32_t vf[2][4]; // v: column `col`, 16 keys each
+    if (sg.n > 0)
+        bring_qk(0);
+    if constexpr (OUT) // scores of later keys: stay 0
+        for (int x = tid; x < 2 * HPW * 2 * 16 * 4; x += NT)
+            *reinterpret_cast<u32x2 *>(&sm_p[x >> 6 & 1][x / 128 % HPW][x / 128 / HPW][(x >> 2 & 15) * PR + 32 +
+                                                                                   (x & 3) * 8]) = u32x2{0u, 0u};
+    // S is there: left to the compiler, every chunk would wait for it, and with it for what is asked for meanwhile
+#pragma unroll
+    for (int t = 0; t < TK; ++t)
+        settle(S[t]);
+    int c = -1, buf = 2; // chunk, and where its q and k are; before the first one what it needs ahead
+    for (int c0 = -C; c0 < sg.n; c0 += C, ++c) {
+        // What the chunk before asked for is in LDS; the stores of its read-outs, two instructions behind
+        // that, may still be on their way.
+        if (OUT && c > 0)
+            asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        lds_barrier();
+        const int next = buf < 2 ? buf + 1 : 0;
+        if (coming_v < sg.n) {
+            bring_v((c + 1) & 1);
+            if (coming < sg.n)
+                bring_qk(next < 2 ? next + 1 : 0);
+            ahead(c0 + C, c + 1, next);
+        }
+        if (c < 0) {
+            buf = next;
+            continue;
+        }
+        const uint8_t *kb = sm_qk[buf], *qb = kb + KB, *vb = sm_v[c & 1];
+        uint32_t vf[2][4]; // this lane's column, 16 keys each
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             transposed(vb + u * 16 * DV * 2 + tv_at[0], vb + u * 16 * DV * 2 + tv_at[1], vf[u]);
 
         if constexpr (OUT) {
-            f32x16 P, O;
+            f32x16 O;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                P[i] = O[i] = 0.f;
+                O[i] = 0.f;
+            const float begin = sm_begin[c & 1][hw][n_];
+            int r_at = row_at; // addresses are formed anew each chunk: kept, they cost 8 registers
+            asm volatile("" : "+v"(r_at));
 #pragma unroll
             for (int t = 0; t < TK; ++t)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int chunk = t * 4 + u * 2 + hh;
-                    const int at = n_ * DK * 2 + ((chunk ^ swizzle<DK>(n_)) * 16);
-                    const bf16x8 qf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(qb + at));
-                    const bf16x8 kf = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(kb + at));
+                    const bf16x8 qf = __builtin_bit_cast(
+                        bf16x8, *reinterpret_cast<const u32x4 *>(qb + (r_at ^ (t * 64 + u * 32))));
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         split2(S[t][8 * u + 2 * e], S[t][8 * u + 2 * e + 1], hi[e], lo[e]);
-                    P = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf, P, 0, 0, 0);
                     O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(hi), qf, O, 0, 0, 0);
                     O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(lo), qf, O, 0, 0, 0);
                 }
-            settle(P);
             settle(O);
-            const float begin = __builtin_amdgcn_exp2f(G_hi + G_lo);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 O[i] *= begin;
-            // An infinity or NaN in v must not reach tokens before it (0 times it is NaN): it leaves this
-            // product, and from its token on the column becomes NaN.
-            bool odd = false;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    odd |= not_finite(vf[u][e]);
+            u16x2 most = {0, 0};
             uint32_t vc[2][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e) {
                     vc[u][e] = vf[u][e];
-            if (__ballot(odd)) {
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, vf[u][e] & 0x7fff7fffu));
+                }
+            // An infinity or NaN in v must not reach tokens before it (0 times it is NaN): it leaves this
+            // product, and from its token on the column becomes NaN.
+            if (__ballot(most[0] >= 0x7f80 || most[1] >= 0x7f80)) {
                 int since = C; // the first such key of this lane's column
 #pragma unroll
                 for (int u = 1; u >= 0; --u)
@@ -375,60 +540,53 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float w[2];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int i = 8 * u + 2 * e + y, key = 8 * (i >> 2) + 4 * hh + (i & 3);
-                        const float d = (G_hi - K_hi[i >> 2][i & 3]) + (G_lo - K_lo[i >> 2][i & 3]);
-                        w[y] = key <= n_ ? P[i] * __builtin_amdgcn_exp2f(d) : 0.f;
-                    }
-                    split2(w[0], w[1], hi[e], lo[e]);
-                }
-                O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), operand(hi), O, 0, 0, 0);
-                O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), operand(lo), O, 0, 0, 0);
+                const u32x4 hi = *reinterpret_cast<const u32x4 *>(&sm_p[c & 1][hw][0][n_ * PR + u * 32 + hh * 16]);
+                const u32x4 lo = *reinterpret_cast<const u32x4 *>(&sm_p[c & 1][hw][1][n_ * PR + u * 32 + hh * 16]);
+                O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), __builtin_bit_cast(bf16x8, hi), O, 0, 0, 0);
+                O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), __builtin_bit_cast(bf16x8, lo), O, 0, 0, 0);
             }
             settle(O);
-            if (n_ < rows) {
-                uint16_t *o = p.out.p + (int64_t)(sg.first + c0 + n_) * p.out.row + (int64_t)hv * p.out.head +
-                              wave * 32 + 8 * hh;
+            if (c0 + n_ < sg.n) {
+                uint16_t *o = p.out.p + (int64_t)(sg.first + c0 + n_) * p.out.row + (int64_t)hv * p.out.head + col0 +
+                              8 * hh;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = pack_bf16(O[8 * u + 2 * e] * p.q_scale, O[8 * u + 2 * e + 1] * p.q_scale);
+                        y[e] = pack_bf16(O[8 * u + 2 * e], O[8 * u + 2 * e + 1]);
                     *reinterpret_cast<u32x4 *>(o + 16 * u) = u32x4{y[0], y[1], y[2], y[3]};
                 }
             }
         }
 
         // the state behind the chunk
+        const float f = sm_f[c & 1][hw];
+        if (__ballot(f != 1.f)) { // uniform
 #pragma unroll
-        for (int t = 0; t < TK; ++t)
-            S[t] *= keep;
+            for (int t = 0; t < TK; ++t)
+                S[t] *= f;
+        }
+        int k_at[2] = {tk_at[0], tk_at[1]};
+        asm volatile("" : "+v"(k_at[0]), "+v"(k_at[1]));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float w[2];
+            for (int x = 0; x < 2; ++x) {
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(&sm_b[c & 1][hw][16 * u + 8 * x + 4 * hh]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int i = 8 * u + 2 * e + y, key = 8 * (i >> 2) + 4 * hh + (i & 3);
-                    const float d = (E_hi - K_hi[i >> 2][i & 3]) + (E_lo - K_lo[i >> 2][i & 3]);
-                    const float v = __uint_as_float(y ? vf[u][e] & 0xffff0000u : vf[u][e] << 16);
-                    w[y] = key < rows ? v * __builtin_amdgcn_exp2f(d) : 0.f;
+                    const int e = 2 * x + y;
+                    split3(__uint_as_float(vf[u][e] << 16) * w[2 * y],
+                           __uint_as_float(vf[u][e] & 0xffff0000u) * w[2 * y + 1], hi[e], mid[e], lo[e]);
                 }
-                split3(w[0], w[1], hi[e], mid[e], lo[e]);
             }
 #pragma unroll
             for (int t = 0; t < TK; ++t) {
                 uint32_t kt[4];
                 const int o = u * 16 * DK * 2, x = t * 64;
-                transposed(kb + o + (tk_at[0] ^ x), kb + o + (tk_at[1] ^ x), kt);
+                transposed(kb + o + (k_at[0] ^ x), kb + o + (k_at[1] ^ x), kt);
                 S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(hi), S[t], 0, 0, 0);
                 S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(mid), S[t], 0, 0, 0);
                 S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(lo), S[t], 0, 0, 0);
@@ -437,14 +595,21 @@ __global__ __launch_bounds__(2 * DV, 2) void lin_prefill_kernel(LinPrefillParams
 #pragma unroll
         for (int t = 0; t < TK; ++t)
             settle(S[t]);
+        buf = next;
+    }
+    if (sg.n > 0) {
+        const float scale = exp2_of(sm_off[(c - 1) & 1][hw]);
+#pragma unroll
+        for (int t = 0; t < TK; ++t)
+            S[t] *= scale;
     }
     if constexpr (OUT) {
         if (last)
             store_state(p.state + ((int64_t)sg.write * p.H_v + hv) * tile);
     } else {
         store_state(p.entry + ((int64_t)(place + 1) * p.H_v + hv) * tile);
-        if (tid == 0)
-            p.decay[(int64_t)(place + 1) * p.H_v + hv] = total;
+        if (wave % WPH == 0 && lane == 0)
+            p.decay[(int64_t)(place + 1) * p.H_v + hv] = exp2_of(sm_total[(c - 1) & 1][hw]);
     }
 }
 
@@ -489,7 +654,7 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinPrefillParams p)
 size_t lin_prefill_layout(int B, int T, int H_v, int d_k, int d_v, void *base, LinPrefillParams *p)
 {
     // tokens of a segment: two waves a SIMD where the call has them
-    const int64_t waves = (int64_t)device_cus() * 8;
+    const int64_t waves = (int64_t)device_cus() * LIN_TARGET;
     int64_t segment = ((int64_t)T * H_v * (d_v / 32) + waves - 1) / waves;
     segment = segment < 128 ? 128 : (segment > 1024 ? 1024 : segment);
     segment = (segment + C - 1) / C * C;
@@ -505,24 +670,33 @@ size_t lin_prefill_layout(int B, int T, int H_v, int d_k, int d_v, void *base, L
     return entry + decay + 256;
 }
 
-template <int DK, int DV>
-static hipError_t launch_prefill(const LinPrefillParams &p, hipStream_t stream)
+template <int DK, int DV, int HPW>
+static hipError_t launch_walk(const LinPrefillParams &p, hipStream_t stream)
 {
     LinPrefillParams q = p;
     void *args[] = {&q};
-    const unsigned grid = (unsigned)(((int64_t)p.segments * p.H_v + 7) / 8 * 8);
+    const dim3 grid((unsigned)(((int64_t)p.segments * (p.H_v / HPW) + 7) / 8 * 8)), block(HPW * DV * 2);
     hipError_t e = hipSuccess;
     if (p.T > p.segment) { // some sequence may have several
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&lin_prefill_kernel<DK, DV, false>), dim3(grid),
-                            dim3(2 * DV), args, 0, stream);
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&lin_prefill_kernel<DK, DV, HPW, false>), grid, block, args,
+                            0, stream);
         if (e == hipSuccess)
             e = hipLaunchKernel(reinterpret_cast<const void *>(&lin_carry_kernel<DK, DV>),
                                 dim3((unsigned)(p.B * p.H_v * (DK * DV / 1024))), dim3(256), args, 0, stream);
     }
     if (e == hipSuccess)
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&lin_prefill_kernel<DK, DV, true>), dim3(grid),
-                            dim3(2 * DV), args, 0, stream);
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&lin_prefill_kernel<DK, DV, HPW, true>), grid, block, args,
+                            0, stream);
     return e;
+}
+
+template <int DK, int DV>
+static hipError_t launch_prefill(const LinPrefillParams &p, hipStream_t stream)
+{
+    if constexpr (DV == 64)
+        if (p.H_v / p.H_k % 2 == 0)
+            return launch_walk<DK, DV, 2>(p, stream);
+    return launch_walk<DK, DV, 1>(p, stream);
 }
 
 hipError_t launch_lin_prefill(const LinPrefillParams &p, int d_k, int d_v, hipStream_t stream)

@@ -602,7 +602,7 @@ gdn_status kv_page_compact(const gdn_pages *pages, int32_t *remap, int32_t *resu
  *   reads q and k of head hv / (H_v / H_k);  d_k, d_v  64 or 128;  N  slots with
  *   the null slot 0;  per_token  g holds 0: a log decay for each head [H_v], 1: one
  *   for each token and head too
- * q, k, v and out by gdn_heads (row strides up to 2^24); out overlaps none of
+ * q, k, v and out by gdn_heads (strides up to 2^24); out overlaps none of
  * them.  state [N][H_v][d_k][d_v] fp32, S[i][j] with i over keys, 16-byte aligned.
  * Log decays below -177 count as -177 (e^-177 is 0 in fp32). */
 typedef struct gdn_lin_dims {
