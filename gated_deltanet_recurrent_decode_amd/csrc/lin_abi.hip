@@ -118,7 +118,7 @@ size_t lin_attn_prefill_workspace_bytes(const gdn_lin_dims *dims)
 {
     if (!dims || check_dims(*dims) != GDN_OK)
         return 0;
-    return gdn::lin_prefill_layout(dims->B, dims->T, dims->H_v, dims->d_k, dims->d_v, nullptr, nullptr);
+    return gdn::lin_prefill_layout(dims->B, dims->T, dims->H_k, dims->H_v, dims->d_k, dims->d_v, nullptr, nullptr);
 }
 
 gdn_status lin_attn_prefill(const gdn_lin_dims *dims, const gdn_heads *q, const gdn_heads *k, const gdn_heads *v,
@@ -141,7 +141,7 @@ gdn_status lin_attn_prefill(const gdn_lin_dims *dims, const gdn_heads *q, const 
     if (!aligned(workspace, 256))
         return GDN_ERR_UNSUPPORTED;
     gdn::LinPrefillParams p{};
-    if (workspace_bytes < gdn::lin_prefill_layout(d.B, d.T, d.H_v, d.d_k, d.d_v, workspace, &p) ||
+    if (workspace_bytes < gdn::lin_prefill_layout(d.B, d.T, d.H_k, d.H_v, d.d_k, d.d_v, workspace, &p) ||
         (int64_t)p.segments * d.H_v >= 1 << 24)
         return GDN_ERR_SHAPE;
     p.q = heads_of(*q);

@@ -30,6 +30,6 @@ struct LinPrefillParams {
 hipError_t launch_lin_step(const LinStepParams &p, int d_k, int d_v, hipStream_t stream);
 hipError_t launch_lin_prefill(const LinPrefillParams &p, int d_k, int d_v, hipStream_t stream);
 // device scratch in bytes; fills the parameter block's pointers and segment sizes when it is given
-size_t lin_prefill_layout(int B, int T, int H_v, int d_k, int d_v, void *base, LinPrefillParams *p);
+size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void *base, LinPrefillParams *p);
 
 } // namespace gdn

@@ -32,8 +32,26 @@ constexpr int C = 32; // tokens of a chunk
 #ifndef LIN_WAVES
 #define LIN_WAVES 2
 #endif
-#ifndef LIN_TARGET
-#define LIN_TARGET 8
+#ifdef LIN_NT
+#define LIN_ST(x, p) __builtin_nontemporal_store(x, p)
+#else
+#define LIN_ST(x, p) (*(p) = (x))
+#endif
+#ifdef LIN_NT2
+#define LIN_ST2(x, p) __builtin_nontemporal_store(x, p)
+#else
+#define LIN_ST2(x, p) (*(p) = (x))
+#endif
+#ifdef LIN_NT3
+#define LIN_ST3(x, p) __builtin_nontemporal_store(x, p)
+#else
+#define LIN_ST3(x, p) (*(p) = (x))
+#endif
+#ifndef LIN_FIXED
+#define LIN_FIXED 160
+#endif
+#ifndef LIN_MAX
+#define LIN_MAX 2048
 #endif
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -198,9 +216,8 @@ __device__ __forceinline__ bf16x8 operand(const uint32_t (&x)[4])
 // OUT: the walk, with read-outs.  Otherwise a segment's own part of the state, for all but a
 // sequence's last.
 //
-// What the waves of a head would all compute is dealt out among them a chunk ahead and goes through LDS: the
-// weighted scores w_ij = q_scale (q_i . k_j) 2^(G_i - G_j), as pairs of bf16 numbers, and the scales of the
-// tokens.  So there is one barrier a chunk.
+// What the waves of a head would all compute is dealt out among them and goes through LDS: the weighted
+// scores w_ij = q_scale (q_i . k_j) 2^(G_i - G_j), as pairs of bf16 numbers, and the scales of the tokens.
 template <int DK, int DV, int HPW, bool OUT>
 __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(LinPrefillParams p)
 {
@@ -209,14 +226,14 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
     constexpr int KB = C * DK * 2, VB = C * DV * 2; // bytes of a chunk's k (and q), of a head's v
     constexpr int QKB = (OUT ? 2 : 1) * KB;
     constexpr int IK = KB / (1024 * NW), IV = HPW * VB / (1024 * NW); // instructions a wave that bring them
-    constexpr int PR = 80; // bytes of a row of scores: 64, and room against bank conflicts
-    __shared__ __align__(16) uint8_t sm_qk[3][QKB], sm_v[2][HPW * VB];
-    __shared__ __align__(16) float sm_g[3][HPW][64];
-    __shared__ __align__(16) uint8_t sm_p[OUT ? 2 : 1][HPW][2][OUT ? C * PR : 16];
-    __shared__ __align__(16) float sm_G[OUT ? NW : 1][2][C]; // a wave's own: sums of log decays
-    __shared__ __align__(16) float sm_begin[2][HPW][C], sm_b[2][HPW][C];
-    __shared__ float sm_f[2][HPW];
-    __shared__ double sm_off[2][HPW], sm_total[2][HPW];
+    constexpr int PR = 64;                          // bytes of a row of scores
+    __shared__ __align__(16) uint8_t sm_qk[2][QKB], sm_v[2][HPW * VB];
+    __shared__ __align__(16) float sm_g[HPW][64];
+    __shared__ __align__(16) uint8_t sm_p[HPW][2][OUT ? C * PR : 16];
+    __shared__ __align__(16) float sm_begin[HPW][C], sm_b[HPW][C];
+    __shared__ float sm_f[HPW];
+    __shared__ double sm_off[HPW], sm_total[HPW];
+    static_assert(HPW * VB >= NW * 2 * C * 4, "room for a wave's sums");
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
@@ -274,7 +291,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
         for (int t = 0; t < TK; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                to[cell_of(t, i)] = S[t][i];
+                LIN_ST(S[t][i], &to[cell_of(t, i)]);
     };
 
     if (!OUT && sg.s == 0) // the walk may find the slot already written: it begins from this copy
@@ -304,47 +321,38 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
         return reinterpret_cast<const uint8_t *>((uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32 |
                                                  (uint32_t)uniform((int)at));
     };
-    int coming = 0, coming_v = 0; // tokens whose q and k, and whose v, were asked for
-    auto bring_qk = [&](int buf) {
-        lds_byte *to = (lds_byte *)sm_qk + buf * QKB + wave * 1024;
-        const int last = sg.n - coming - 1;
+    auto bring = [&](int buf, int c0) {
+        const int last = sg.n - c0 - 1;
         if (last < C - 1) {
 #pragma unroll
             for (int i = 0; i < IK; ++i) {
                 off_k[i] = offset(width_k, p.k, i, last);
                 off_q[i] = offset(width_k, p.q, i, last);
             }
-        }
-        const uint8_t *base_k = base_of(p.k, hk, coming);
-#pragma unroll
-        for (int i = 0; i < IK; ++i)
-            load_to_lds(to + i * NW * 1024, base_k, off_k[i]);
-        if constexpr (OUT) {
-            const uint8_t *base_q = base_of(p.q, hk, coming);
-#pragma unroll
-            for (int i = 0; i < IK; ++i)
-                load_to_lds(to + KB + i * NW * 1024, base_q, off_q[i]);
-        }
-        if (wave < HPW) { // the decays, a wave a head
-            const int t = coming + (n_ < last ? n_ : last), h = h0 + wave;
-            load_dword_to_lds((lds_byte *)sm_g + (buf * HPW + wave) * 256,
-                              p.g + (p.per_token ? (int64_t)(sg.first + t) * p.H_v + h : (int64_t)h));
-        }
-        coming += C;
-    };
-    auto bring_v = [&](int buf) {
-        lds_byte *to = (lds_byte *)sm_v + buf * (HPW * VB) + wave * 1024;
-        const int last = sg.n - coming_v - 1;
-        if (last < C - 1) {
 #pragma unroll
             for (int i = 0; i < IV; ++i)
                 off_v[i] = offset(width_v, p.v, i, last);
         }
-        const uint8_t *base_v = base_of(p.v, h0, coming_v);
+        lds_byte *to = (lds_byte *)sm_qk + buf * QKB + wave * 1024;
+        const uint8_t *base_k = base_of(p.k, hk, c0), *base_v = base_of(p.v, h0, c0);
+#pragma unroll
+        for (int i = 0; i < IK; ++i)
+            load_to_lds(to + i * NW * 1024, base_k, off_k[i]);
+        if constexpr (OUT) {
+            const uint8_t *base_q = base_of(p.q, hk, c0);
+#pragma unroll
+            for (int i = 0; i < IK; ++i)
+                load_to_lds(to + KB + i * NW * 1024, base_q, off_q[i]);
+        }
+        to = (lds_byte *)sm_v + buf * (HPW * VB) + wave * 1024;
 #pragma unroll
         for (int i = 0; i < IV; ++i)
             load_to_lds(to + i * NW * 1024, base_v, off_v[i]);
-        coming_v += C;
+        if (wave < HPW) { // the decays, a wave a head
+            const int t = c0 + (n_ < last ? n_ : last), h = h0 + wave;
+            load_dword_to_lds((lds_byte *)sm_g + wave * 256,
+                              p.g + (p.per_token ? (int64_t)(sg.first + t) * p.H_v + h : (int64_t)h));
+        }
     };
 
     // transposing reads: lane (hv, r, c) points at key 4 hv + r (+ 8 for the second), columns 4 c
@@ -371,32 +379,35 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
     // + sum_j w_ij v_j and S~ += k_j (2^(-L_j) v_j)^T, with no decay of the whole state, until some |L_i| of
     // a chunk passes kRange.  There S~ takes the scale of the chunk's end, 2^(off + G_end), and off is -G_end
     // for its weights.
-    auto sums = [&](int c0, int buf, int head) { // G of this lane's token
+    auto sums = [&](int c0, int head) { // G of this lane's token
         const int rows = sg.n - c0 < C ? sg.n - c0 : C;
-        return scan32(n_ < rows ? (double)log2_decay(sm_g[buf][head][n_]) : 0.0);
+        return scan32(n_ < rows ? (double)log2_decay(sm_g[head][n_]) : 0.0);
     };
-    auto scales = [&](int c0, int c, int buf, int head) { // of chunk c, at token c0
-        const double G = sums(c0, buf, head), end = lane_value(G, C - 1);
-        const double off = c > 0 ? sm_off[(c - 1) & 1][head] : 0.0, total = c > 0 ? sm_total[(c - 1) & 1][head] : 0.0;
+    auto scales = [&](int c0, int head) { // of the chunk at token c0
+        const double G = sums(c0, head), end = lane_value(G, C - 1);
+        const double off = c0 > 0 ? sm_off[head] : 0.0, total = c0 > 0 ? sm_total[head] : 0.0;
         const bool far = __ballot(fabs(off + G) > (double)kRange) != 0;
         const double base = far ? -end : off;
         if (hh == 0) {
-            sm_begin[c & 1][head][n_] = exp2_of(off + G) * p.q_scale;
-            sm_b[c & 1][head][n_] = c0 + n_ < sg.n ? exp2_of(-(base + G)) : 0.f;
+            sm_begin[head][n_] = exp2_of(off + G) * p.q_scale;
+            sm_b[head][n_] = c0 + n_ < sg.n ? exp2_of(-(base + G)) : 0.f;
         }
         if (lane == 0) {
-            sm_f[c & 1][head] = far ? exp2_of(off + end) : 1.f;
-            sm_off[c & 1][head] = base + end;
-            sm_total[c & 1][head] = total + end;
+            sm_f[head] = far ? exp2_of(off + end) : 1.f;
+            sm_off[head] = base + end;
+            sm_total[head] = total + end;
         }
     };
+    // A row of scores: its 16-byte chunk x of 4, at another place every two rows (32 lanes read 32 rows).
+    auto score_at = [](int row, int x) { return row * PR + ((x ^ (row >> 1 & 3)) * 16); };
     // the scores of keys 16 kt.. and tokens 16 tt.., 16 x 16 x 32 products: a lane has a token and four keys
-    auto scores = [&](int c0, int c, int buf, int head, int kt, int tt) {
-        const double G = sums(c0, buf, head);
+    auto scores = [&](int c0, int buf, int head, int kt, int tt) {
+        const double G = sums(c0, head);
         const float G_hi = (float)G, G_lo = (float)(G - (double)G_hi);
+        float *own = reinterpret_cast<float *>(sm_v[buf ^ 1]) + wave * 2 * C; // nobody reads v there any more
         if (hh == 0) {
-            sm_G[wave][0][n_] = G_hi;
-            sm_G[wave][1][n_] = G_lo;
+            own[n_] = G_hi;
+            own[C + n_] = G_lo;
         }
         const int m = lane & 15, g4 = lane >> 4;
         const uint8_t *kb = sm_qk[buf], *qb = kb + KB;
@@ -411,9 +422,9 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
         }
         settle(P);
         __builtin_amdgcn_wave_barrier();
-        const float T_hi = sm_G[wave][0][16 * tt + m], T_lo = sm_G[wave][1][16 * tt + m];
-        const f32x4 K_hi = *reinterpret_cast<const f32x4 *>(&sm_G[wave][0][16 * kt + 4 * g4]);
-        const f32x4 K_lo = *reinterpret_cast<const f32x4 *>(&sm_G[wave][1][16 * kt + 4 * g4]);
+        const float T_hi = own[16 * tt + m], T_lo = own[C + 16 * tt + m];
+        const f32x4 K_hi = *reinterpret_cast<const f32x4 *>(&own[16 * kt + 4 * g4]);
+        const f32x4 K_lo = *reinterpret_cast<const f32x4 *>(&own[C + 16 * kt + 4 * g4]);
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -427,53 +438,42 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
         split2(w[2], w[3], x, y);
         hi[1] = x, lo[1] = y;
         // keys in the order of the product with v: blocks of four, 0 2 1 3
-        const int at = (16 * tt + m) * PR + kt * 32 + ((g4 & 1) * 2 + (g4 >> 1)) * 8;
-        *reinterpret_cast<u32x2 *>(&sm_p[c & 1][head][0][at]) = hi;
-        *reinterpret_cast<u32x2 *>(&sm_p[c & 1][head][1][at]) = lo;
+        const int at = score_at(16 * tt + m, 2 * kt + (g4 & 1)) + (g4 >> 1) * 8;
+        *reinterpret_cast<u32x2 *>(&sm_p[head][0][at]) = hi;
+        *reinterpret_cast<u32x2 *>(&sm_p[head][1][at]) = lo;
         __builtin_amdgcn_wave_barrier();
-    };
-    auto ahead = [&](int c0, int c, int buf) {
-        constexpr int JOBS = OUT ? 4 : 1; // a head
-        for (int job = wave; job < JOBS * HPW; job += NW) {
-            const int head = job / JOBS, x = job % JOBS;
-            if (x == JOBS - 1)
-                scales(c0, c, buf, head);
-            else if constexpr (OUT)
-                scores(c0, c, buf, head, x == 2, x > 0);
-        }
     };
 
     if (sg.n > 0)
-        bring_qk(0);
+        bring(0, 0);
     if constexpr (OUT) // scores of later keys: stay 0
-        for (int x = tid; x < 2 * HPW * 2 * 16 * 4; x += NT)
-            *reinterpret_cast<u32x2 *>(&sm_p[x >> 6 & 1][x / 128 % HPW][x / 128 / HPW][(x >> 2 & 15) * PR + 32 +
-                                                                                   (x & 3) * 8]) = u32x2{0u, 0u};
+        for (int x = tid; x < HPW * 2 * 16 * 4; x += NT)
+            *reinterpret_cast<u32x2 *>(&sm_p[x >> 7][x >> 6 & 1][score_at(x >> 2 & 15, 2 + (x >> 1 & 1)) + (x & 1) * 8]) =
+                u32x2{0u, 0u};
     // S is there: left to the compiler, every chunk would wait for it, and with it for what is asked for meanwhile
 #pragma unroll
     for (int t = 0; t < TK; ++t)
         settle(S[t]);
-    int c = -1, buf = 2; // chunk, and where its q and k are; before the first one what it needs ahead
-    for (int c0 = -C; c0 < sg.n; c0 += C, ++c) {
-        // What the chunk before asked for is in LDS; the stores of its read-outs, two instructions behind
-        // that, may still be on their way.
-        if (OUT && c > 0)
+    for (int c0 = 0, buf = 0; c0 < sg.n; c0 += C, buf ^= 1) {
+        // The chunk is in LDS; the stores of the read-outs before it, two instructions behind its loads, may
+        // still be on their way.
+        if (OUT && c0 > 0)
             asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
         else
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
-        const int next = buf < 2 ? buf + 1 : 0;
-        if (coming_v < sg.n) {
-            bring_v((c + 1) & 1);
-            if (coming < sg.n)
-                bring_qk(next < 2 ? next + 1 : 0);
-            ahead(c0 + C, c + 1, next);
+        constexpr int JOBS = OUT ? 4 : 1; // a head
+        for (int job = wave; job < JOBS * HPW; job += NW) {
+            const int head = job / JOBS, x = job % JOBS;
+            if (x == JOBS - 1)
+                scales(c0, head);
+            else if constexpr (OUT)
+                scores(c0, buf, head, x == 2, x > 0);
         }
-        if (c < 0) {
-            buf = next;
-            continue;
-        }
-        const uint8_t *kb = sm_qk[buf], *qb = kb + KB, *vb = sm_v[c & 1];
+        lds_barrier();
+        if (c0 + C < sg.n) // every wave is past the chunk before this one
+            bring(buf ^ 1, c0 + C);
+        const uint8_t *kb = sm_qk[buf], *qb = kb + KB, *vb = sm_v[buf];
         uint32_t vf[2][4]; // this lane's column, 16 keys each
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 O[i] = 0.f;
-            const float begin = sm_begin[c & 1][hw][n_];
+            const float begin = sm_begin[hw][n_];
             int r_at = row_at; // addresses are formed anew each chunk: kept, they cost 8 registers
             asm volatile("" : "+v"(r_at));
 #pragma unroll
@@ -540,8 +540,8 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const u32x4 hi = *reinterpret_cast<const u32x4 *>(&sm_p[c & 1][hw][0][n_ * PR + u * 32 + hh * 16]);
-                const u32x4 lo = *reinterpret_cast<const u32x4 *>(&sm_p[c & 1][hw][1][n_ * PR + u * 32 + hh * 16]);
+                const u32x4 hi = *reinterpret_cast<const u32x4 *>(&sm_p[hw][0][score_at(n_, 2 * u + hh)]);
+                const u32x4 lo = *reinterpret_cast<const u32x4 *>(&sm_p[hw][1][score_at(n_, 2 * u + hh)]);
                 O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), __builtin_bit_cast(bf16x8, hi), O, 0, 0, 0);
                 O = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(vc[u]), __builtin_bit_cast(bf16x8, lo), O, 0, 0, 0);
             }
@@ -555,13 +555,13 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         y[e] = pack_bf16(O[8 * u + 2 * e], O[8 * u + 2 * e + 1]);
-                    *reinterpret_cast<u32x4 *>(o + 16 * u) = u32x4{y[0], y[1], y[2], y[3]};
+                    LIN_ST3((u32x4{y[0], y[1], y[2], y[3]}), reinterpret_cast<u32x4 *>(o + 16 * u));
                 }
             }
         }
 
         // the state behind the chunk
-        const float f = sm_f[c & 1][hw];
+        const float f = sm_f[hw];
         if (__ballot(f != 1.f)) { // uniform
 #pragma unroll
             for (int t = 0; t < TK; ++t)
@@ -574,7 +574,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
             uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const f32x4 w = *reinterpret_cast<const f32x4 *>(&sm_b[c & 1][hw][16 * u + 8 * x + 4 * hh]);
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(&sm_b[hw][16 * u + 8 * x + 4 * hh]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int e = 2 * x + y;
@@ -595,10 +595,9 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
 #pragma unroll
         for (int t = 0; t < TK; ++t)
             settle(S[t]);
-        buf = next;
     }
     if (sg.n > 0) {
-        const float scale = exp2_of(sm_off[(c - 1) & 1][hw]);
+        const float scale = exp2_of(sm_off[hw]);
 #pragma unroll
         for (int t = 0; t < TK; ++t)
             S[t] *= scale;
@@ -609,7 +608,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
     } else {
         store_state(p.entry + ((int64_t)(place + 1) * p.H_v + hv) * tile);
         if (wave % WPH == 0 && lane == 0)
-            p.decay[(int64_t)(place + 1) * p.H_v + hv] = exp2_of(sm_total[(c - 1) & 1][hw]);
+            p.decay[(int64_t)(place + 1) * p.H_v + hv] = exp2_of(sm_total[hw]);
     }
 }
 
@@ -646,18 +645,41 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinPrefillParams p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[e] = fmaf(d[i], x[e], u[i][e]);
-                at[(s + i - 1) * step] = x;
+                LIN_ST2(x, &at[(s + i - 1) * step]);
             }
     }
 }
 
-size_t lin_prefill_layout(int B, int T, int H_v, int d_k, int d_v, void *base, LinPrefillParams *p)
+// Workgroups of the walk that a CU holds: by their LDS with d_k = 64, by registers or LDS with 128.
+static int walks_a_cu(int d_k, int d_v, bool pair)
 {
-    // tokens of a segment: two waves a SIMD where the call has them
-    const int64_t waves = (int64_t)device_cus() * LIN_TARGET;
-    int64_t segment = ((int64_t)T * H_v * (d_v / 32) + waves - 1) / waves;
-    segment = segment < 128 ? 128 : (segment > 1024 ? 1024 : segment);
-    segment = (segment + C - 1) / C * C;
+    if (d_k == 64)
+        return d_v == 128 ? 4 : (pair ? 3 : 5);
+    return d_v == 128 || pair ? 2 : 3;
+}
+
+size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void *base, LinPrefillParams *p)
+{
+    // Tokens of a segment: the shortest ones that give at most `rounds` times the workgroups that the chip holds
+    // at once, sequences' last ones counted as whole, with the rounds that cost least.  A workgroup's start and end
+    // and its state's way through memory cost about as much as kFixed tokens.
+    constexpr int64_t kFixed = LIN_FIXED;
+    const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
+    const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);
+    int64_t segment = 0, least = 0;
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+        const int64_t most = rounds * slots / groups; // segments: (T + B (L - 1)) / L of them at most
+        if (most < B || T < B)
+            continue;
+        int64_t L = (T - B) / (most - B + 1) + 1;
+        L = ((L < 4 * C ? 4 * C : L) + C - 1) / C * C;
+        if (least == 0 || rounds * (L + kFixed) < least) {
+            least = rounds * (L + kFixed);
+            segment = L;
+        }
+    }
+    if (segment == 0 || segment > LIN_MAX)
+        segment = LIN_MAX;
     const int64_t segments = T / segment + B;
     const size_t entry = T > segment ? round256((size_t)segments * H_v * d_k * d_v * 4) : 0;
     const size_t decay = T > segment ? round256((size_t)segments * H_v * 4) : 0;
