@@ -29,30 +29,6 @@ namespace gdn {
 namespace {
 
 constexpr int C = 32; // tokens of a chunk
-#ifndef LIN_WAVES
-#define LIN_WAVES 2
-#endif
-#ifdef LIN_NT
-#define LIN_ST(x, p) __builtin_nontemporal_store(x, p)
-#else
-#define LIN_ST(x, p) (*(p) = (x))
-#endif
-#ifdef LIN_NT2
-#define LIN_ST2(x, p) __builtin_nontemporal_store(x, p)
-#else
-#define LIN_ST2(x, p) (*(p) = (x))
-#endif
-#ifdef LIN_NT3
-#define LIN_ST3(x, p) __builtin_nontemporal_store(x, p)
-#else
-#define LIN_ST3(x, p) (*(p) = (x))
-#endif
-#ifndef LIN_FIXED
-#define LIN_FIXED 160
-#endif
-#ifndef LIN_MAX
-#define LIN_MAX 2048
-#endif
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -219,7 +195,7 @@ __device__ __forceinline__ bf16x8 operand(const uint32_t (&x)[4])
 // What the waves of a head would all compute is dealt out among them and goes through LDS: the weighted
 // scores w_ij = q_scale (q_i . k_j) 2^(G_i - G_j), as pairs of bf16 numbers, and the scales of the tokens.
 template <int DK, int DV, int HPW, bool OUT>
-__global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(LinPrefillParams p)
+__global__ __launch_bounds__(HPW *DV * 2, 2) void lin_prefill_kernel(LinPrefillParams p)
 {
     constexpr int WPH = DV / 32, NW = WPH * HPW, NT = 64 * NW;
     constexpr int TK = DK / 32;                     // 32-row tiles of S
@@ -227,13 +203,13 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
     constexpr int QKB = (OUT ? 2 : 1) * KB;
     constexpr int IK = KB / (1024 * NW), IV = HPW * VB / (1024 * NW); // instructions a wave that bring them
     constexpr int PR = 64;                          // bytes of a row of scores
-    __shared__ __align__(16) uint8_t sm_qk[2][QKB], sm_v[2][HPW * VB];
+    __shared__ __align__(16) uint8_t sm_qk[2][QKB], sm_v[2][HPW * VB]; // a chunk, and the next on its way
     __shared__ __align__(16) float sm_g[HPW][64];
     __shared__ __align__(16) uint8_t sm_p[HPW][2][OUT ? C * PR : 16];
     __shared__ __align__(16) float sm_begin[HPW][C], sm_b[HPW][C];
     __shared__ float sm_f[HPW];
     __shared__ double sm_off[HPW], sm_total[HPW];
-    static_assert(HPW * VB >= NW * 2 * C * 4, "room for a wave's sums");
+    static_assert(!OUT || HPW * VB >= NW * 2 * C * 4, "room for a wave's sums");
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
@@ -291,7 +267,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
         for (int t = 0; t < TK; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                LIN_ST(S[t][i], &to[cell_of(t, i)]);
+                to[cell_of(t, i)] = S[t][i];
     };
 
     if (!OUT && sg.s == 0) // the walk may find the slot already written: it begins from this copy
@@ -555,7 +531,7 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         y[e] = pack_bf16(O[8 * u + 2 * e], O[8 * u + 2 * e + 1]);
-                    LIN_ST3((u32x4{y[0], y[1], y[2], y[3]}), reinterpret_cast<u32x4 *>(o + 16 * u));
+                    *reinterpret_cast<u32x4 *>(o + 16 * u) = u32x4{y[0], y[1], y[2], y[3]};
                 }
             }
         }
@@ -582,15 +558,21 @@ __global__ __launch_bounds__(HPW *DV * 2, LIN_WAVES) void lin_prefill_kernel(Lin
                            __uint_as_float(vf[u][e] & 0xffff0000u) * w[2 * y + 1], hi[e], mid[e], lo[e]);
                 }
             }
+            uint32_t kt[TK][4];
 #pragma unroll
             for (int t = 0; t < TK; ++t) {
-                uint32_t kt[4];
                 const int o = u * 16 * DK * 2, x = t * 64;
-                transposed(kb + o + (k_at[0] ^ x), kb + o + (k_at[1] ^ x), kt);
-                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(hi), S[t], 0, 0, 0);
-                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(mid), S[t], 0, 0, 0);
-                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt), operand(lo), S[t], 0, 0, 0);
+                transposed(kb + o + (k_at[0] ^ x), kb + o + (k_at[1] ^ x), kt[t]);
             }
+#pragma unroll
+            for (int t = 0; t < TK; ++t)
+                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt[t]), operand(hi), S[t], 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < TK; ++t)
+                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt[t]), operand(mid), S[t], 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < TK; ++t)
+                S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(kt[t]), operand(lo), S[t], 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < TK; ++t)
@@ -645,7 +627,7 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinPrefillParams p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[e] = fmaf(d[i], x[e], u[i][e]);
-                LIN_ST2(x, &at[(s + i - 1) * step]);
+                at[(s + i - 1) * step] = x;
             }
     }
 }
@@ -663,7 +645,7 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
     // Tokens of a segment: the shortest ones that give at most `rounds` times the workgroups that the chip holds
     // at once, sequences' last ones counted as whole, with the rounds that cost least.  A workgroup's start and end
     // and its state's way through memory cost about as much as kFixed tokens.
-    constexpr int64_t kFixed = LIN_FIXED;
+    constexpr int64_t kFixed = 160, kMost = 2048;
     const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
     const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);
     int64_t segment = 0, least = 0;
@@ -678,8 +660,8 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
             segment = L;
         }
     }
-    if (segment == 0 || segment > LIN_MAX)
-        segment = LIN_MAX;
+    if (segment == 0 || segment > kMost)
+        segment = kMost;
     const int64_t segments = T / segment + B;
     const size_t entry = T > segment ? round256((size_t)segments * H_v * d_k * d_v * 4) : 0;
     const size_t decay = T > segment ? round256((size_t)segments * H_v * 4) : 0;
