@@ -18,7 +18,8 @@ __all__ = ["GdnError", "lib", "gdn_decode_step", "gdn_decode_step_commit", "gdn_
            "NOALLOC_SCRATCH_BYTES", "conv_decode",
            "slot_commit",
            "slot_reset", "slot_copy", "check_slots", "traffic_probe", "status_string", "LIB_PATH", "EXPORTS",
-           "rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "kv_page_workspace_bytes",
+           "rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "attn_shared",
+           "attn_shared_workspace_bytes", "kv_page_workspace_bytes",
            "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact",
            "lin_attn_step", "lin_attn_step_tokens", "lin_attn_prefill", "lin_attn_prefill_workspace_bytes"]
 
@@ -546,8 +547,8 @@ def traffic_probe(state, read_slot, write_slot, sink, *, traffic: str = "copy", 
 # ------------------------------------------------------------------ the full-attention layers
 
 from . import attention as _attention  # noqa: E402  (it takes this module's helpers)
-from .attention import (attn_paged, attn_paged_workspace_bytes, attn_prologue, kv_page_compact,  # noqa: E402
-                        kv_page_copy, kv_page_fork, kv_page_free, kv_page_reserve, kv_page_workspace_bytes,
+from .attention import (attn_paged, attn_paged_workspace_bytes, attn_prologue, attn_shared,  # noqa: E402
+                        attn_shared_workspace_bytes, kv_page_compact, kv_page_copy, kv_page_fork, kv_page_free, kv_page_reserve, kv_page_workspace_bytes,
                         rope_freqs)
 
 EXPORTS += _attention.EXPORTS

@@ -15,7 +15,8 @@ import struct
 
 from . import GdnError, _check, lib
 
-EXPORTS = ("gdn_rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "kv_page_workspace_bytes",
+EXPORTS = ("gdn_rope_freqs", "attn_prologue", "attn_paged", "attn_paged_workspace_bytes", "attn_shared",
+           "attn_shared_workspace_bytes", "kv_page_workspace_bytes",
            "kv_page_reserve", "kv_page_fork", "kv_page_free", "kv_page_copy", "kv_page_compact")
 ROPE_STRETCH = {"none": 0, "linear": 1, "base": 2, "wavelength": 3}
 
@@ -66,6 +67,8 @@ def declare(L) -> None:
             ("attn_prologue", [_P] * 12, _i32),
             ("attn_paged", [_P, _P, _P, _P, _P, _P, _P, _f32, _P, size, _P], _i32),
             ("attn_paged_workspace_bytes", [_P], size),
+            ("attn_shared", [_P] * 7 + [_i32, _P, _P, _f32, _P, size, _P], _i32),
+            ("attn_shared_workspace_bytes", [_P, _i32], size),
             ("kv_page_workspace_bytes", [_i32, _i32, _i32], size),
             ("kv_page_reserve", [_P, _P, _P, _i32, _P, _P, size, _P], _i32),
             ("kv_page_fork", [_P, _P, _P, _i32, _P, _P, size, _P], _i32),
@@ -318,6 +321,45 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
             _heads(q, "q", T, H_q, d, bf, dev),
             _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
             _at(cu_seqlens, "cu_seqlens", i32, dev), _heads(out, "out", T, H_q, d, bf, dev),
+            _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
+            _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
+
+
+def attn_shared_workspace_bytes(B: int, T: int, K: int, max_new: int, H_q: int, H_kv: int, d: int) -> int:
+    """The workspace attn_shared needs for K groups (see include/gdn.h), in bytes, on the current GPU."""
+    n = lib().attn_shared_workspace_bytes(_DIMS.pack(B, T, 1, H_q, H_kv, d, 1, 16, 1, max_new, 0, 0), K)
+    if n == 0:
+        raise GdnError("attn_shared_workspace_bytes", 2)
+    return n
+
+
+def attn_shared(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, cu_groups, shared_len, out, workspace, *,
+                max_new: int, scale: float | None = None, window: int = 0, lse=None, k_scale=None, v_scale=None,
+                stream=None) -> None:
+    """attn_paged for sequences that share prefixes, which are read once a group (see ``attn_shared`` in
+    include/gdn.h).
+
+    cu_groups [K+1] and shared_len [K] int32: sequences cu_groups[g] .. cu_groups[g+1]-1 have the same first
+    shared_len[g] positions; workspace a uint8 tensor of attn_shared_workspace_bytes; the rest as attn_paged."""
+    torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
+    N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
+    B = _packed_layout(row, cu_seqlens)
+    T, H_q = _packed_heads(q, "q")
+    if page_table is None:
+        raise ValueError("page_table is required")
+    if lse is not None and lse.shape != (T, H_q):
+        raise ValueError("lse must be [T][H_q]")
+    groups = shared_len.shape
+    if len(groups) != 1 or cu_groups.shape != (groups[0] + 1,):
+        raise ValueError("shared_len must be [K] and cu_groups [K+1]")
+    dev = _gpu(q, "q")
+    _launch("attn_shared", lib().attn_shared, dev, stream,
+            _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind),
+            _heads(q, "q", T, H_q, d, bf, dev),
+            _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
+            _at(cu_seqlens, "cu_seqlens", i32, dev), _at(cu_groups, "cu_groups", i32, dev),
+            _at(shared_len, "shared_len", i32, dev), groups[0], _heads(out, "out", T, H_q, d, bf, dev),
             _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
             _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
 

@@ -55,6 +55,62 @@ gdn_status check_cache(const gdn_kv_cache &c, bool e4m3)
     return !aligned(c.k, 16) || !aligned(c.v, 16) ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
+constexpr int32_t kMostGroups = 1024; // of a call: a planning workgroup's threads
+
+// What the attention calls share; on GDN_OK with *run set p holds all but the workspace (*run is false when there
+// is nothing to do).
+gdn_status attn_setup(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
+                      const int32_t *cu_seqlens, const gdn_heads *out, float *lse, float scale, void *workspace,
+                      gdn::AttnParams &p, bool *run)
+{
+    *run = false;
+
+    if (!dims)
+        return GDN_ERR_NULL;
+    const gdn_attn_dims d = *dims;
+    if (d.B == 0 || d.T == 0)
+        return GDN_OK;
+    if (!q || !q->data || !out || !out->data || !cache || !cache->page_table || !cache->kv_len || !row ||
+        !cu_seqlens || !workspace)
+        return GDN_ERR_NULL;
+    gdn_status st = check_dims(d);
+    if (st != GDN_OK)
+        return st;
+    if ((st = check_cache(*cache, d.cache_type == 1)) != GDN_OK || (st = check_heads(*q)) != GDN_OK ||
+        (st = check_heads(*out)) != GDN_OK)
+        return st;
+    if (!aligned(workspace, 256) || !aligned(lse, 4))
+        return GDN_ERR_UNSUPPORTED;
+    if (!isfinite(scale))
+        return GDN_ERR_SHAPE;
+    p.q = heads_of(*q);
+    p.out = heads_of(*out);
+    p.lse = lse;
+    p.k_pages = cache->k;
+    p.v_pages = cache->v;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.page_table = cache->page_table;
+    p.kv_len = cache->kv_len;
+    p.row = row;
+    p.cu = cu_seqlens;
+    p.scale = scale * 1.44269504088896340736f;
+    p.B = d.B;
+    p.T = d.T;
+    p.R = d.R;
+    p.H_q = d.H_q;
+    p.H_kv = d.H_kv;
+    p.G = d.H_q / d.H_kv;
+    p.N = d.N;
+    p.page_shift = page_shift(d.page_size);
+    p.width = d.table_width;
+    p.max_new = d.max_new;
+    // no position lies further back than the table reaches; the kernels add to a window in 32 bits
+    p.window = d.window < (int64_t)d.table_width * d.page_size ? d.window : 0;
+    *run = true;
+    return GDN_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -175,52 +231,48 @@ gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_k
                       const int32_t *cu_seqlens, const gdn_heads *out, float *lse, float scale, void *workspace,
                       size_t workspace_bytes, hipStream_t stream)
 {
-    if (!dims)
-        return GDN_ERR_NULL;
-    const gdn_attn_dims d = *dims;
-    if (d.B == 0 || d.T == 0)
-        return GDN_OK;
-    if (!q || !q->data || !out || !out->data || !cache || !cache->page_table || !cache->kv_len || !row ||
-        !cu_seqlens || !workspace)
-        return GDN_ERR_NULL;
-    gdn_status st = check_dims(d);
-    if (st != GDN_OK)
-        return st;
-    if ((st = check_cache(*cache, d.cache_type == 1)) != GDN_OK || (st = check_heads(*q)) != GDN_OK ||
-        (st = check_heads(*out)) != GDN_OK)
-        return st;
-    if (!aligned(workspace, 256) || !aligned(lse, 4))
-        return GDN_ERR_UNSUPPORTED;
-    if (!isfinite(scale))
-        return GDN_ERR_SHAPE;
     gdn::AttnParams p{};
-    if (workspace_bytes < gdn::attn_paged_layout(d.B, d.T, d.max_new, d.H_kv, d.H_q / d.H_kv, d.d, workspace, &p))
+    bool run;
+    const gdn_status st = attn_setup(dims, q, cache, row, cu_seqlens, out, lse, scale, workspace, p, &run);
+    if (st != GDN_OK || !run)
+        return st;
+    if (workspace_bytes < gdn::attn_paged_layout(p.B, p.T, p.max_new, p.H_kv, p.G, dims->d, workspace, &p))
         return GDN_ERR_SHAPE;
-    p.q = heads_of(*q);
-    p.out = heads_of(*out);
-    p.lse = lse;
-    p.k_pages = cache->k;
-    p.v_pages = cache->v;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
-    p.page_table = cache->page_table;
-    p.kv_len = cache->kv_len;
-    p.row = row;
-    p.cu = cu_seqlens;
-    p.scale = scale * 1.44269504088896340736f;
-    p.B = d.B;
-    p.T = d.T;
-    p.R = d.R;
-    p.H_q = d.H_q;
-    p.H_kv = d.H_kv;
-    p.G = d.H_q / d.H_kv;
-    p.N = d.N;
-    p.page_shift = page_shift(d.page_size);
-    p.width = d.table_width;
-    p.max_new = d.max_new;
-    // no position lies further back than the table reaches; the kernels add to a window in 32 bits
-    p.window = d.window < (int64_t)d.table_width * d.page_size ? d.window : 0;
-    return from_hip(gdn::launch_attn_paged(p, d.d, d.cache_type == 1, stream));
+    return from_hip(gdn::launch_attn_paged(p, dims->d, dims->cache_type == 1, stream));
+}
+
+size_t attn_shared_workspace_bytes(const gdn_attn_dims *dims, int32_t groups)
+{
+    if (!dims || groups < 0 || groups > kMostGroups)
+        return 0;
+    const gdn_attn_dims d = *dims;
+    if (d.B < 0 || d.T < 0 || d.max_new < 0 || d.H_q < 1 || d.H_kv < 1 || d.H_q % d.H_kv != 0 ||
+        (d.d != 64 && d.d != 128 && d.d != 256))
+        return 0;
+    return gdn::attn_shared_layout(d.B, d.T, groups, d.max_new, d.H_kv, d.H_q / d.H_kv, d.d, nullptr, nullptr);
+}
+
+gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
+                       const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
+                       const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream)
+{
+    gdn::AttnParams p{};
+    bool run;
+    const gdn_status st = attn_setup(dims, q, cache, row, cu_seqlens, out, lse, scale, workspace, p, &run);
+    if (st != GDN_OK || !run)
+        return st;
+    if (groups < 0 || groups > kMostGroups)
+        return GDN_ERR_SHAPE;
+    if (groups > 0 && (!cu_groups || !shared_len))
+        return GDN_ERR_NULL;
+    if (((int64_t)p.T * p.G / 256 + groups) * p.H_kv > INT32_MAX / 4 ||
+        workspace_bytes < gdn::attn_shared_layout(p.B, p.T, groups, p.max_new, p.H_kv, p.G, dims->d, workspace, &p))
+        return GDN_ERR_SHAPE;
+    p.cu_groups = groups > 0 ? cu_groups : nullptr;
+    p.shared_len = shared_len;
+    p.K = groups;
+    return from_hip(gdn::launch_attn_shared(p, dims->d, dims->cache_type == 1, stream));
 }
 
 size_t kv_page_workspace_bytes(int32_t n, int32_t R, int32_t N)

@@ -40,6 +40,11 @@ struct AttnParams {
     int32_t *count;             // tiles: entries, and from [2] on their units in 64 bits
     int capacity;               // tiles: entries that the workspace holds
     int block;                  // tiles: keys of a block
+    // a batch that shares prefixes
+    const int32_t *cu_groups, *shared_len; // [K + 1], [K]
+    int K;
+    int own_blocks;             // 32-row blocks of a part of a sequence's own keys
+    int64_t shared_parts;       // where the parts of shared keys begin, in 32-row blocks
 };
 
 struct PageParams {
@@ -63,6 +68,10 @@ size_t attn_rows_layout(int d, void *base, AttnParams *p);
 size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnParams *p);
 hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
 hipError_t launch_attn_tiles(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
+size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int d, void *base, AttnParams *p);
+// the tiles of a plan with shared entries (attn_tiles.hip), and the whole call
+hipError_t launch_attn_tiles_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
+hipError_t launch_attn_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
 hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream);
 hipError_t launch_kv_reserve(const PageParams &p, hipStream_t stream);
 hipError_t launch_kv_fork(const PageParams &p, hipStream_t stream);

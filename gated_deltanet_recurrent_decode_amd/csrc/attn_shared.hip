@@ -1,0 +1,334 @@
+// attn_shared.hip -- paged attention for a batch whose rows share long prefixes (gfx950).
+//
+// The keys of a row fall into those that its group has in common and its own.  A softmax over both is joined
+// from its parts: with (o, m, l) of each, weights relative to its maximum m and their sum l,
+//   m = max(m_a, m_b),  l = l_a e^(m_a - m) + l_b e^(m_b - m),  o = (o_a e^(m_a - m) + o_b e^(m_b - m)) / l.
+// The rows of a group lie behind each other, so for the common keys they are one sequence: tiles of 256 (token,
+// head of the group) rows that read each key once, where the rows by themselves would read it once each.  The
+// tiles of attn_tiles.hip do both kinds of entries in one launch, dealt out by the key over all workgroups: a
+// first kernel lists the sequences' own entries and then the groups', a last one joins each row's parts.
+//
+// What a group has in common is found on the device: the length that the call gives, cut to what every usable
+// member has before its new tokens, and to whole 16 keys (a block's staging rows lie on one page so).  Longer or
+// shorter, the result is the same; only what is read once changes.
+
+#include "attn_tiles.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+namespace {
+
+// A group's keys are taken together from this many on: below, its rows' second parts cost more than the
+// keys that they read again.
+constexpr int kLeastShared = 128;
+
+// The last x of n with first[x] <= v, the first at least.
+__device__ __forceinline__ int last_at(const int *first, int n, int v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+} // namespace
+
+__global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int own_capacity, int shared_capacity)
+{
+    __shared__ int g_begin[PT + 1], g_len[PT], g_low[PT], g_row[PT], g_members[PT], g_entry[PT], g_tiles[PT],
+        g_first[PT], g_tokens[PT];
+    __shared__ int first_entry[PT + 1];
+    __shared__ Seq seqs[PT];
+    const int tid = threadIdx.x;
+    if (tid < p.K) {
+        const int at = p.cu_groups[tid];
+        g_begin[tid] = at < 0 ? 0 : (at > p.B ? p.B : at);
+        g_len[tid] = p.shared_len[tid];
+        g_low[tid] = g_row[tid] = 0x7fffffff;
+        g_members[tid] = 0;
+    }
+    if (tid == 0) {
+        const int at = p.cu_groups ? p.cu_groups[p.K] : 0;
+        g_begin[p.K] = at < 0 ? 0 : (at > p.B ? p.B : at);
+    }
+    __syncthreads();
+    auto group_of = [&](int b) { // or -1
+        if (p.K == 0)
+            return -1;
+        const int g = last_at(g_begin, p.K, b);
+        return b >= g_begin[g] && b < g_begin[g + 1] ? g : -1;
+    };
+    for (int b = tid; b < p.B; b += PT) {
+        const Seq s = read_seq(p, b);
+        const int g = s.kind == kNormal ? group_of(b) : -1;
+        if (g >= 0) {
+            atomicMin(&g_len[g], s.L - s.n);
+            atomicMin(&g_low[g], p.window > 0 ? s.L - s.n - p.window + 1 : 0);
+            atomicMin(&g_row[g], b); // read through its first usable member
+            atomicAdd(&g_members[g], 1);
+        }
+    }
+    __syncthreads();
+    int mine = 0;
+    if (tid < p.K) {
+        const int first = p.cu[g_begin[tid]], tokens = p.cu[g_begin[tid + 1]] - first;
+        const int len = g_len[tid] > 0 ? g_len[tid] & ~15 : 0, low = g_low[tid] > 0 ? g_low[tid] & ~15 : 0;
+        const bool ok = g_members[tid] > 1 && g_begin[tid] < g_begin[tid + 1] && len - low >= kLeastShared &&
+                        first >= 0 && tokens > 0 && first + tokens <= p.T;
+        g_len[tid] = ok ? len : 0;
+        g_low[tid] = low;
+        g_row[tid] = ok ? p.row[g_row[tid]] : 0;
+        g_first[tid] = first;
+        g_tokens[tid] = tokens;
+        g_tiles[tid] = ok ? (int)(((int64_t)tokens * p.G + TR - 1) / TR) : 0;
+        mine = g_tiles[tid] * p.H_kv;
+    }
+    // groups that overlap have more tiles than the workspace was sized for: what is past its end is left out
+    long long sum_groups;
+    const long long group_at = plan_scan((long long)mine, &sum_groups);
+    const int shared_entries = sum_groups < shared_capacity ? (int)sum_groups : shared_capacity;
+    if (tid < p.K)
+        g_entry[tid] = group_at < shared_entries ? (int)group_at : shared_entries;
+
+    // the sequences' own keys
+    int entries = 0;
+    long long units = 0;
+    for (int b0 = 0; b0 < p.B; b0 += PT) {
+        const int b = b0 + tid;
+        int mine = 0;
+        __syncthreads(); // the round before has read the tables
+        if (b < p.B) {
+            Seq s = read_seq(p, b);
+            mine = tiles_of(p, s) * p.H_kv;
+            const int g = s.kind == kNormal ? group_of(b) : -1;
+            s.lo = g >= 0 && g_len[g] > 0 ? g + 1 : 0; // for now its group
+            seqs[tid] = s;
+        }
+        long long sum_all;
+        const long long mine_at = plan_scan((long long)mine, &sum_all);
+        const int room = own_capacity - entries, all = sum_all < room ? (int)sum_all : room;
+        first_entry[tid] = mine_at < all ? (int)mine_at : all;
+        if (tid == 0)
+            first_entry[PT] = all;
+        __syncthreads();
+        for (int e0 = 0; e0 < all; e0 += PT) {
+            const int e = e0 + tid;
+            long long u = 0;
+            int h = 0, tile = 0, g = -1;
+            Seq s{};
+            if (e < all) {
+                const int q = last_at(first_entry, PT, e);
+                s = seqs[q];
+                g = s.lo - 1;
+                s.lo = g >= 0 ? g_len[g] : 0;
+                const int tiles = tiles_of(p, s), x = e - first_entry[q];
+                h = x / tiles;
+                tile = x - h * tiles;
+                u = span_of<true>(p, s, tile).blocks;
+            }
+            long long sum;
+            const long long at = units + plan_scan(u, &sum);
+            if (e < all) {
+                const int64_t o = entries + e;
+                p.before[o] = at;
+                i32x4 *to = reinterpret_cast<i32x4 *>(p.entry + o * kSharedEntry);
+                to[0] = i32x4{h, tile, s.kind, s.first};
+                to[1] = i32x4{s.n, s.L, s.r, s.lo};
+                to[2] = g >= 0 ? i32x4{g_first[g], g_entry[g], g_tiles[g], 0} : i32x4{0, 0, 0, 0};
+            }
+            units += sum;
+        }
+        entries += all;
+    }
+    // the groups' common keys
+    const int own_entries = entries;
+    for (int e0 = 0; e0 < shared_entries; e0 += PT) {
+        const int e = e0 + tid;
+        long long u = 0;
+        int g = 0, h = 0, tile = 0;
+        if (e < shared_entries) {
+            g = last_at(g_entry, p.K, e);
+            const int x = e - g_entry[g], tiles = g_tiles[g] > 0 ? g_tiles[g] : 1;
+            h = x / tiles;
+            tile = x - h * tiles;
+            u = (g_len[g] - g_low[g] + p.block - 1) / p.block;
+        }
+        long long sum;
+        const long long at = units + plan_scan(u, &sum);
+        if (e < shared_entries) {
+            const int64_t o = entries + e;
+            p.before[o] = at;
+            i32x4 *to = reinterpret_cast<i32x4 *>(p.entry + o * kSharedEntry);
+            to[0] = i32x4{h, tile, kShared, g_first[g]};
+            to[1] = i32x4{g_tokens[g], g_len[g], g_row[g], g_low[g]};
+        }
+        units += sum;
+    }
+    entries += shared_entries;
+    if (tid == 0) {
+        p.before[entries] = units;
+        p.count[0] = entries;
+        p.count[1] = own_entries;
+        *reinterpret_cast<long long *>(p.count + 2) = units;
+    }
+}
+
+// blockIdx.x = an entry of a sequence's own keys; a wave 32 rows by 32 columns of it, a lane 16 values of a row as
+// the tiles had them in their registers.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256) void attn_shared_join_kernel(AttnParams p)
+{
+    constexpr int DT = D / 32, BATCH = 2;
+    const int lane = threadIdx.x & 63, n_ = lane & 31, hh = lane >> 5;
+    const int item = uniform(blockIdx.y * 4 + (threadIdx.x >> 6)), blk = item / DT, a = item % DT;
+    const int e = blockIdx.x, own_entries = p.count[1];
+    if (e >= own_entries)
+        return;
+    const int32_t *entry = p.entry + (int64_t)e * kSharedEntry;
+    const int h = entry[0], tile = entry[1], kind = entry[2], first = entry[3], rows = entry[4] * p.G, lo = entry[7];
+    if (kind != kNormal || tile * TR + blk * 32 >= rows)
+        return;
+    const long long total = *reinterpret_cast<const long long *>(p.count + 2);
+    const int pieces = pieces_of(p, total);
+    const int w0 = owner_of(total, p.before[e], pieces), w1 = owner_of(total, p.before[e + 1] - 1, pieces);
+    if (lo == 0 && w0 == w1)
+        return; // whole, and it shares nothing: written by the tiles
+    const int row = tile * TR + blk * 32 + n_;
+    const bool valid = row < rows;
+    float m = neg_inf(), l = 0.f;
+    f32x4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // parts w_a .. w_b of a row: at(w) their 32-row block, r the row in it
+    auto join = [&](int w_a, int w_b, int r, auto at) {
+        for (int w = w_a; w <= w_b; w += BATCH) {
+            f32x2 ml[BATCH];
+            f32x4 po[BATCH][4];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int64_t part = at(w + k <= w_b ? w + k : w);
+                ml[k] = *reinterpret_cast<const f32x2 *>(p.part_ml + (part * 32 + r) * 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    po[k][i] = *reinterpret_cast<const f32x4 *>(p.part_o + part * 32 * D + a * 1024 + i * 256 +
+                                                                (hh * 32 + r) * 4);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                top = fmaxf(top, ml[k][0]);
+            const float safe = top == neg_inf() ? 0.f : top;
+            const float keep = __builtin_amdgcn_exp2f(m - safe);
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] *= keep;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (w + k <= w_b) {
+                    const float f = __builtin_amdgcn_exp2f(ml[k][0] - safe);
+                    l = fmaf(ml[k][1], f, l);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i >> 2][i & 3] = fmaf(po[k][i >> 2][i & 3], f, o[i >> 2][i & 3]);
+                }
+            }
+            m = top;
+        }
+    };
+    if (lo > 0 && valid) { // the row's place among its group's
+        const int64_t at = (int64_t)(first - entry[8]) * p.G + row;
+        const int es = own_entries + entry[9] + h * entry[10] + (int)(at / TR);
+        if (es < p.count[0])
+            join(owner_of(total, p.before[es], pieces), owner_of(total, p.before[es + 1] - 1, pieces), (int)(at % 32),
+                 [&](int w) { return shared_part(p, es, own_entries, w) + at % TR / 32; });
+    }
+    join(w0, w1, n_, [&](int w) { return own_part(p, e, w) + blk; });
+    if (!valid)
+        return;
+    const int64_t t = first + row / p.G;
+    const int hq = h * p.G + row % p.G;
+    const float vs = E4M3 ? p.v_scale[h] : 1.0f;
+    const float inv = l == 0.f ? 0.f : vs / l;
+    uint16_t *out = p.out.p + t * p.out.row + (int64_t)hq * p.out.head + a * 32 + 4 * hh;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2 *>(out + 8 * i) =
+            u32x2{pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv)};
+    if (a == 0 && hh == 0 && p.lse)
+        p.lse[t * p.H_q + hq] = lse_of(m, l);
+}
+
+namespace {
+
+struct Sizes {
+    size_t own, shared; // entries
+    int own_blocks;     // 32-row blocks of an own part
+};
+
+Sizes sizes_of(int B, int T, int K, int max_new, int H_kv, int G)
+{
+    const int64_t rows = (int64_t)max_new * G;
+    return Sizes{((size_t)T * G / TR + B) * H_kv, ((size_t)T * G / TR + K) * H_kv,
+                 rows >= TR ? TR / 32 : (rows > 32 ? (int)((rows + 31) / 32) : 1)};
+}
+
+} // namespace
+
+size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)
+{
+    const Sizes s = sizes_of(B, T, K, max_new, H_kv, G);
+    const int workgroups = (device_cus() + 7) / 8 * 8;
+    const size_t own = (s.own + workgroups) * s.own_blocks, blocks = own + (s.shared + workgroups) * NW;
+    const size_t o = round256(blocks * 32 * d * 4), ml = round256(blocks * 32 * 2 * 4),
+                 bf = round256((s.own + s.shared + 1) * 8), en = round256((s.own + s.shared) * kSharedEntry * 4);
+    if (p) {
+        char *at = static_cast<char *>(base);
+        p->workgroups = workgroups;
+        p->own_blocks = s.own_blocks;
+        p->shared_parts = (int64_t)own;
+        p->part_o = reinterpret_cast<float *>(at);
+        p->part_ml = reinterpret_cast<float *>(at + o);
+        p->before = reinterpret_cast<long long *>(at + o + ml);
+        p->entry = reinterpret_cast<int32_t *>(at + o + ml + bf);
+        p->count = reinterpret_cast<int32_t *>(at + o + ml + bf + en);
+    }
+    return o + ml + bf + en + 256;
+}
+
+template <int D, bool E4M3>
+static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
+{
+    const Sizes s = sizes_of(p.B, p.T, p.K, p.max_new, p.H_kv, p.G);
+    AttnParams q = p;
+    q.block = block_keys(D);
+    int own = (int)s.own, shared = (int)s.shared;
+    void *plan[] = {&q, &own, &shared}, *args[] = {&q};
+    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_shared_plan_kernel), dim3(1), dim3(PT), plan, 0,
+                                   stream);
+    if (e == hipSuccess)
+        e = launch_attn_tiles_shared(p, D, E4M3, stream);
+    if (e == hipSuccess)
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_shared_join_kernel<D, E4M3>),
+                            dim3((unsigned)s.own, (unsigned)((s.own_blocks * (D / 32) + 3) / 4)), dim3(256), args, 0,
+                            stream);
+    return e;
+}
+
+hipError_t launch_attn_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
+{
+    if (d == 64)
+        return e4m3 ? launch_de<64, true>(p, stream) : launch_de<64, false>(p, stream);
+    if (d == 128)
+        return e4m3 ? launch_de<128, true>(p, stream) : launch_de<128, false>(p, stream);
+    return e4m3 ? launch_de<256, true>(p, stream) : launch_de<256, false>(p, stream);
+}
+
+} // namespace gdn

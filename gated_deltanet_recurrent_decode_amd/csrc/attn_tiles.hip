@@ -47,53 +47,16 @@
 // score products (844).  A step's first LDS reads before the step: the same.  64 rows a
 // wave, and blocks of 64 keys at 256 columns: spills.
 
-#include "attn_common.h"
+#include "attn_tiles.h"
 #include "gdn_internal.h"
 
 namespace gdn {
 
 namespace {
 
-constexpr int TR = 256;  // rows of a tile
-// keys of a block: with 256 columns the queries take half of the LDS
-constexpr int block_keys(int d) { return d == 256 ? 32 : 128; }
-constexpr int NW = TR / 32; // waves
-constexpr int NT = 64 * NW;
-constexpr int PT = 1024; // the planning workgroup
-// what the plan says of an entry: kv head, tile, and its sequence, so that nobody reads the lengths again
-constexpr int kEntry = 8;
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
-
-// What a tile of a sequence sees: keys lo .. hi - 1, in blocks from lo on.
-struct Span {
-    int lo, hi, blocks, min_pos, max_pos;
-};
-
-__device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int tile)
-{
-    Span x;
-    const int rows = s.n * p.G;
-    const int last = (rows < (tile + 1) * TR ? rows : (tile + 1) * TR) - 1;
-    x.min_pos = s.L - s.n + tile * TR / p.G;
-    x.max_pos = s.L - s.n + last / p.G;
-    x.hi = s.kind == kNormal && x.max_pos >= 0 ? x.max_pos + 1 : 0;
-    x.lo = 0;
-    if (p.window > 0 && x.min_pos - p.window + 1 > 0)
-        x.lo = (x.min_pos - p.window + 1) & ~(p.block - 1);
-    x.lo = x.lo < x.hi ? x.lo : (x.hi > 0 ? (x.hi - 1) & ~(p.block - 1) : 0);
-    x.blocks = x.hi > x.lo ? (x.hi - x.lo + p.block - 1) / p.block : 1;
-    return x;
-}
-
-__device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s)
-{
-    return s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TR - 1) / TR);
-}
 
 // 16 bytes a lane from base + off into LDS, lane after lane from `to` on.  As inline assembly
 // because the compiler, given the builtin, waits for it before any read of LDS: the loads of the
@@ -105,6 +68,21 @@ __device__ __forceinline__ void load_to_lds(lds_byte *to, const uint8_t *base, i
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)at)), "v"(off),
                  "s"(base)
                  : "memory"); // m0 is reserved: whatever of the compiler's own needs it sets it first
+}
+
+// The first position that token t sees, by its sequence's length and the window.
+__device__ __forceinline__ int first_seen(const AttnParams &p, int t)
+{
+    int lo = 0, hi = p.B; // the last sequence that does not begin behind it
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Seq s = read_seq(p, lo);
+    return s.kind == kNormal ? s.L - s.n + (t - s.first) - p.window + 1 : 0x3fffffff;
 }
 
 // The entry that holds unit u (before[e] <= u < before[e + 1]): 64 probes a round.
@@ -121,33 +99,6 @@ __device__ __forceinline__ int entry_of(const long long *before, int count, long
         hi = lo + step < hi ? lo + step : hi;
     }
     return lo;
-}
-
-// Exclusive sum over the planning workgroup.
-template <class T>
-__device__ __forceinline__ T plan_scan(T v, T *total)
-{
-    __shared__ T wave_sum[PT / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T inc = v;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const T o = __shfl_up(inc, m);
-        if (lane >= m)
-            inc += o;
-    }
-    __syncthreads();
-    if (lane == 63)
-        wave_sum[wave] = inc;
-    __syncthreads();
-    T before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < PT / 64; ++w) {
-        before += w < wave ? wave_sum[w] : 0;
-        all += wave_sum[w];
-    }
-    *total = all;
-    return before + inc - v;
 }
 
 } // namespace
@@ -197,7 +148,7 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
                 const int tiles = tiles_of(p, s), x = e - first_entry[q];
                 h = x / tiles;
                 tile = x - h * tiles;
-                u = span_of(p, s, tile).blocks;
+                u = span_of<false>(p, s, tile).blocks;
             }
             long long sum;
             const long long at = units + plan_scan(u, &sum);
@@ -219,7 +170,8 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
     }
 }
 
-template <int D, bool E4M3>
+// SHARED: of a plan with shared prefixes (attn_shared.hip).
+template <int D, bool E4M3, bool SHARED>
 __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 {
     constexpr int CH = D / 8;                 // chunks of a row
@@ -237,6 +189,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
     __shared__ int sm_odd[2];
     __shared__ __align__(8) uint8_t sm_lost[2][8]; // a block's 16-key parts whose page is outside the pool
     __shared__ u32x4 sm_q[QL ? NW * QL * 64 : 1];
+    __shared__ int sm_reach[SHARED ? TR : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n_ = lane & 31, hh = lane >> 5;
@@ -245,7 +198,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
     // consecutive pieces on one XCD (workgroups go round the eight): they share keys in its L2
     const int per = p.workgroups / 8;
     const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (tid == 0)
+    if (!SHARED && tid == 0)
         write_cut(p, w, Cut{-1});
     const int pieces = pieces_of(p, total);
     if (w >= pieces)
@@ -270,28 +223,45 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
     }
 
     while (u < u_end) {
-        const int32_t *entry = p.entry + (int64_t)e * kEntry;
+        const int32_t *entry = p.entry + (int64_t)e * (SHARED ? kSharedEntry : kEntry);
         const int h = uniform(entry[0]), tile = uniform(entry[1]);
-        const Seq s{uniform(entry[2]), uniform(entry[3]), uniform(entry[4]), uniform(entry[5]), 0, uniform(entry[6])};
+        const Seq s{uniform(entry[2]), uniform(entry[3]), uniform(entry[4]), uniform(entry[5]),
+                    SHARED ? uniform(entry[7]) : 0, uniform(entry[6])};
         const long long t0 = p.before[e], t1 = p.before[e + 1];
-        const Span span = span_of(p, s, tile);
+        const Span span = span_of<SHARED>(p, s, tile);
         const long long stop = t1 < u_end ? t1 : u_end;
         const int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
         const bool whole = u == t0 && stop == t1;
         const int slot = u == u_begin ? 0 : 1;
-        if (tid == 0 && u == t0 && stop < t1)
+        if (!SHARED && tid == 0 && u == t0 && stop < t1)
             write_cut(p, w, Cut{owner_of(total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, tile});
+        const int at_e = e;
         u = stop;
         ++e;
 
         const int rows = s.n * p.G;
         const int row0 = tile * TR + wave * 32; // this wave's first
-        const bool any = row0 < rows && s.kind == kNormal;
+        const bool common = SHARED && s.kind == kShared; // keys that all rows see, but for a window
+        const bool any = row0 < rows && (s.kind == kNormal || common);
         const int row = row0 + n_; // this lane's
-        const int pos = row < rows && s.kind == kNormal ? s.L - s.n + row / p.G : -1;
-        const int reach = p.window > 0 ? p.window - 1 : 0x3fffffff; // a row sees keys pos - reach .. pos
+        int pos = row < rows && s.kind == kNormal ? s.L - s.n + row / p.G : -1;
+        const int uniform_reach = p.window > 0 ? p.window - 1 : 0x3fffffff; // a row sees keys pos - reach .. pos
         const int row1 = (rows < row0 + 32 ? rows : row0 + 32) - 1;
-        const int min_pos = uniform(s.L - s.n + row0 / p.G), max_pos = uniform(any ? s.L - s.n + row1 / p.G : -1);
+        int min_pos = uniform(s.L - s.n + row0 / p.G), max_pos = uniform(any ? s.L - s.n + row1 / p.G : -1);
+        // keys up to `edge` are behind some row's window, those up to `gone` behind every row's
+        int edge = p.window > 0 ? max_pos - p.window : -1, gone = p.window > 0 ? min_pos - p.window : -1;
+        if (common) {
+            pos = row < rows ? s.L - 1 : -1;
+            min_pos = s.L - 1;
+            max_pos = any ? s.L - 1 : -1;
+            gone = -1;
+            if (p.window > 0) {
+                edge = 0x7fffffff;
+                if (hh == 0) // in LDS: with 256 columns registers are short
+                    sm_reach[wave * 32 + n_] = row < rows ? s.L - 1 - first_seen(p, s.first + row / p.G) : -1;
+            }
+        }
+        auto reach_of = [&]() { return SHARED && common && p.window > 0 ? sm_reach[wave * 32 + n_] : uniform_reach; };
 
         // scores are masked before they are scaled, so the scale has to be positive: a negative
         // one moves its sign into q, zero makes q zero
@@ -451,7 +421,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
             }
         };
         auto sees = [&](int key0) { // some row of the wave sees some key of the block
-            return any && key0 <= max_pos && !(p.window > 0 && key0 + SB - 1 <= min_pos - p.window);
+            return any && key0 <= max_pos && key0 + SB - 1 > gone;
         };
         for (int blk = blk0; blk < end; ++blk) {
             const int buf = (blk - blk0) & 1, block0 = span.lo + blk * KB;
@@ -466,7 +436,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
             // A block that some row does not see whole: v of keys past the sequence's last is cleared,
             // and so are infinities and NaN, which 0 times would carry into rows that do not see them.
             bool odd = false;
-            if (block0 + KB - 1 > span.min_pos || (p.window > 0 && block0 <= span.max_pos - p.window)) {
+            if (block0 + KB - 1 > span.min_pos || (p.window > 0 && (common || block0 <= span.max_pos - p.window))) {
                 if (tid == 0)
                     sm_odd[buf ^ 1] = 0;
 #pragma unroll
@@ -500,7 +470,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                     __builtin_amdgcn_s_setprio(0);
                     int v_at[2] = {v_base[0], v_base[1]};
                     asm volatile("" : "+v"(v_at[0]), "+v"(v_at[1]));
-                    const bool mixed = key0 + SB - 1 > min_pos || (p.window > 0 && key0 <= max_pos - p.window);
+                    const bool mixed = key0 + SB - 1 > min_pos || key0 <= edge;
                     const uint8_t *vb = sm_v[buf] + sub * SB * ROWB;
                     f32x16 sc[NS];
                     score(sm_k[buf] + sub * SB * ROWB, sc);
@@ -530,13 +500,14 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                     asm volatile("" : "+v"(lost)); // waited for here, not before the scores
                     if (__ballot(lost != 0)) {
 #pragma unroll
-                        for (int q = 0; q < SB / 16; ++q)
+                        for (int q = 0, reach = reach_of(); q < SB / 16; ++q)
                             bad |= (lost >> (8 * q) & 1) && pos >= key0 + 16 * q &&
                                            pos - reach <= key0 + 16 * q + 15
                                        ? 1
                                        : 0;
                     }
                     if (mixed) {
+                        const int reach = reach_of();
 #pragma unroll
                         for (int y = 0; y < NS; ++y)
 #pragma unroll
@@ -568,6 +539,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                         m = m_new;
                     }
                     if (odd) { // uniform: what left v goes to the rows that see it
+                        const int reach = reach_of();
 #pragma unroll 1
                         for (int j = 0; j < SB && key0 + j < s.L; ++j) {
                             const uint8_t *v = static_cast<const uint8_t *>(p.v_pages) +
@@ -644,7 +616,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
         if (row < rows) {
             const int64_t tk = s.first + row / p.G;
             const int head = h * p.G + row % p.G;
-            if (whole) {
+            if (whole && (!SHARED || (!common && s.lo == 0))) {
                 const float vs = E4M3 ? p.v_scale[h] : 1.0f;
                 const float inv = l == 0.f ? 0.f : vs / l;
                 uint16_t *o = p.out.p + tk * p.out.row + (int64_t)head * p.out.head + 4 * hh;
@@ -659,7 +631,9 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
                     p.lse[tk * p.H_q + head] = lse_of(m, l);
             } else {
                 // as it lies in the registers, 1 KiB a store; the join reads it so
-                const int64_t part = ((int64_t)w * 2 + slot) * NW + wave;
+                int64_t part = ((int64_t)w * 2 + slot) * NW + wave;
+                if constexpr (SHARED)
+                    part = wave + (common ? shared_part(p, at_e, p.count[1], w) : own_part(p, at_e, w));
                 float *o = p.part_o + part * 32 * D + lane * 4;
 #pragma unroll
                 for (int a = 0; a < DT; ++a)
@@ -775,12 +749,31 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_plan_kernel), dim3(1), dim3(PT), args, 0,
                                    stream);
     if (e == hipSuccess)
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3>),
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, false>),
                             dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_join_kernel<D, E4M3>),
                             dim3((unsigned)p.workgroups, NW * (D / 32) / 4), dim3(256), args, 0, stream);
     return e;
+}
+
+template <int D, bool E4M3>
+static hipError_t launch_shared(const AttnParams &p, hipStream_t stream)
+{
+    AttnParams q = p;
+    q.block = block_keys(D);
+    void *args[] = {&q};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, true>),
+                           dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
+}
+
+hipError_t launch_attn_tiles_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
+{
+    if (d == 64)
+        return e4m3 ? launch_shared<64, true>(p, stream) : launch_shared<64, false>(p, stream);
+    if (d == 128)
+        return e4m3 ? launch_shared<128, true>(p, stream) : launch_shared<128, false>(p, stream);
+    return e4m3 ? launch_shared<256, true>(p, stream) : launch_shared<256, false>(p, stream);
 }
 
 hipError_t launch_attn_tiles(const AttnParams &p, int d, bool e4m3, hipStream_t stream)

@@ -511,6 +511,31 @@ gdn_status attn_paged(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_k
 size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
 
 /*
+ * attn_shared -- attn_paged for a batch whose rows share long prefixes (kv_page_fork
+ * leaves them so): sequences cu_groups[g] .. cu_groups[g+1]-1 form group g of `groups`,
+ * and the first shared_len[g] positions of its rows hold the same cells, whichever
+ * pages they lie on; their keys are read once for the whole group, through the row of
+ * its first usable sequence (the rest of each row through its own).  Every sequence's
+ * result is that of attn_paged; its weights are rounded to bf16 at any max_new (o off by
+ * 0.0023 of its norm).  A shared length that is longer than what a usable member has
+ * before its new tokens counts as that, a negative one as 0; a sequence may be in no
+ * group.  A row that reads the common positions through a page outside [1, N) gets
+ * NaN in o and lse; the other members' entries for them are not looked at.
+ * cu_groups [groups + 1] and shared_len [groups] int32 on the device (NULL with groups
+ * 0); 0 <= groups <= 1024.  Preconditions, not checked: cu_groups is non-decreasing in
+ * [0, B]; the common cells agree.  workspace: attn_shared_workspace_bytes(dims, groups)
+ * bytes.  The rest, and statuses, as attn_paged (GDN_ERR_SHAPE also for groups).
+ */
+gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
+                       const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
+                       const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/* The workspace attn_shared needs for dims (B, T, max_new, H_q, H_kv, d) and groups; 0
+ * when dims is NULL or a size is unusable. */
+size_t attn_shared_workspace_bytes(const gdn_attn_dims *dims, int32_t groups);
+
+/*
  * The cache's pages: which are free, who shares them, and moving them.  refs
  * [N] int32 counts the table entries that name a page (0: free; refs[0] of the
  * null page is ignored).  Bookkeeping runs on the device in stream order like
