@@ -46,6 +46,10 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
     __shared__ int first_entry[PT + 1];
     __shared__ Seq seqs[PT];
     const int tid = threadIdx.x;
+    // the first round's sequences, on their way while the groups are read
+    Seq own{kSkip};
+    if (tid < p.B)
+        own = read_seq(p, tid);
     if (tid < p.K) {
         const int at = p.cu_groups[tid];
         g_begin[tid] = at < 0 ? 0 : (at > p.B ? p.B : at);
@@ -65,7 +69,7 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         return b >= g_begin[g] && b < g_begin[g + 1] ? g : -1;
     };
     for (int b = tid; b < p.B; b += PT) {
-        const Seq s = read_seq(p, b);
+        const Seq s = b == tid ? own : read_seq(p, b);
         const int g = s.kind == kNormal ? group_of(b) : -1;
         if (g >= 0) {
             atomicMin(&g_len[g], s.L - s.n);
@@ -86,7 +90,7 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         g_row[tid] = ok ? p.row[g_row[tid]] : 0;
         g_first[tid] = first;
         g_tokens[tid] = tokens;
-        g_tiles[tid] = ok ? (int)(((int64_t)tokens * p.G + TR - 1) / TR) : 0;
+        g_tiles[tid] = ok ? (int)(((int64_t)tokens * p.G + p.tile_rows - 1) / p.tile_rows) : 0;
         mine = g_tiles[tid] * p.H_kv;
     }
     // groups that overlap have more tiles than the workspace was sized for: what is past its end is left out
@@ -104,8 +108,8 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         int mine = 0;
         __syncthreads(); // the round before has read the tables
         if (b < p.B) {
-            Seq s = read_seq(p, b);
-            mine = tiles_of(p, s) * p.H_kv;
+            Seq s = b0 == 0 ? own : read_seq(p, b);
+            mine = tiles_of(p, s, p.tile_rows) * p.H_kv;
             const int g = s.kind == kNormal ? group_of(b) : -1;
             s.lo = g >= 0 && g_len[g] > 0 ? g + 1 : 0; // for now its group
             seqs[tid] = s;
@@ -127,10 +131,10 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
                 s = seqs[q];
                 g = s.lo - 1;
                 s.lo = g >= 0 ? g_len[g] : 0;
-                const int tiles = tiles_of(p, s), x = e - first_entry[q];
+                const int tiles = tiles_of(p, s, p.tile_rows), x = e - first_entry[q];
                 h = x / tiles;
                 tile = x - h * tiles;
-                u = span_of<true>(p, s, tile).blocks;
+                u = span_of<true>(p, s, tile, p.tile_rows).blocks;
             }
             long long sum;
             const long long at = units + plan_scan(u, &sum);
@@ -179,80 +183,90 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
     }
 }
 
-// blockIdx.x = an entry of a sequence's own keys; a wave 32 rows by 32 columns of it, a lane 16 values of a row as
-// the tiles had them in their registers.
+// blockIdx.x = an entry of a sequence's own keys, blockIdx.y 32 rows by 32 columns of it: a lane has 16 values of a row
+// as the tiles had them in their registers.  Four waves take every fourth part and meet in LDS.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void attn_shared_join_kernel(AttnParams p)
 {
-    constexpr int DT = D / 32, BATCH = 2;
-    const int lane = threadIdx.x & 63, n_ = lane & 31, hh = lane >> 5;
-    const int item = uniform(blockIdx.y * 4 + (threadIdx.x >> 6)), blk = item / DT, a = item % DT;
+    constexpr int DT = D / 32, JW = 4;
+    __shared__ f32x2 sm_ml[JW][64];
+    __shared__ f32x4 sm_o[JW][4][64];
+    const int lane = threadIdx.x & 63, n_ = lane & 31, hh = lane >> 5, wave = uniform(threadIdx.x >> 6);
+    const int blk = blockIdx.y / DT, a = blockIdx.y % DT;
     const int e = blockIdx.x, own_entries = p.count[1];
     if (e >= own_entries)
         return;
     const int32_t *entry = p.entry + (int64_t)e * kSharedEntry;
     const int h = entry[0], tile = entry[1], kind = entry[2], first = entry[3], rows = entry[4] * p.G, lo = entry[7];
-    if (kind != kNormal || tile * TR + blk * 32 >= rows)
+    const int tr = p.tile_rows;
+    if (kind != kNormal || tile * tr + blk * 32 >= rows)
         return;
     const long long total = *reinterpret_cast<const long long *>(p.count + 2);
     const int pieces = pieces_of(p, total);
     const int w0 = owner_of(total, p.before[e], pieces), w1 = owner_of(total, p.before[e + 1] - 1, pieces);
     if (lo == 0 && w0 == w1)
         return; // whole, and it shares nothing: written by the tiles
-    const int row = tile * TR + blk * 32 + n_;
+    const int row = tile * tr + blk * 32 + n_;
     const bool valid = row < rows;
     float m = neg_inf(), l = 0.f;
     f32x4 o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // parts w_a .. w_b of a row: at(w) their 32-row block, r the row in it
+    auto add = [&](f32x2 ml, const f32x4(&x)[4]) {
+        const float top = fmaxf(m, ml[0]), safe = top == neg_inf() ? 0.f : top;
+        const float keep = __builtin_amdgcn_exp2f(m - safe), f = __builtin_amdgcn_exp2f(ml[0] - safe);
+        l = fmaf(ml[1], f, l * keep);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[i >> 2][i & 3] = fmaf(x[i >> 2][i & 3], f, o[i >> 2][i & 3] * keep);
+        m = top;
+    };
+    // this wave's of the parts w_a .. w_b of a row: at(w) their 32-row block, r the row in it
     auto join = [&](int w_a, int w_b, int r, auto at) {
-        for (int w = w_a; w <= w_b; w += BATCH) {
+        constexpr int BATCH = 2;
+        for (int w = w_a + wave; w <= w_b; w += JW * BATCH) {
             f32x2 ml[BATCH];
             f32x4 po[BATCH][4];
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                const int64_t part = at(w + k <= w_b ? w + k : w);
+                const int64_t part = at(w + k * JW <= w_b ? w + k * JW : w);
                 ml[k] = *reinterpret_cast<const f32x2 *>(p.part_ml + (part * 32 + r) * 2);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     po[k][i] = *reinterpret_cast<const f32x4 *>(p.part_o + part * 32 * D + a * 1024 + i * 256 +
                                                                 (hh * 32 + r) * 4);
             }
-            float top = m;
 #pragma unroll
             for (int k = 0; k < BATCH; ++k)
-                top = fmaxf(top, ml[k][0]);
-            const float safe = top == neg_inf() ? 0.f : top;
-            const float keep = __builtin_amdgcn_exp2f(m - safe);
-            l *= keep;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] *= keep;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                if (w + k <= w_b) {
-                    const float f = __builtin_amdgcn_exp2f(ml[k][0] - safe);
-                    l = fmaf(ml[k][1], f, l);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i >> 2][i & 3] = fmaf(po[k][i >> 2][i & 3], f, o[i >> 2][i & 3]);
-                }
-            }
-            m = top;
+                if (w + k * JW <= w_b)
+                    add(ml[k], po[k]);
         }
     };
     if (lo > 0 && valid) { // the row's place among its group's
         const int64_t at = (int64_t)(first - entry[8]) * p.G + row;
-        const int es = own_entries + entry[9] + h * entry[10] + (int)(at / TR);
+        const int es = own_entries + entry[9] + h * entry[10] + (int)(at / tr);
         if (es < p.count[0])
             join(owner_of(total, p.before[es], pieces), owner_of(total, p.before[es + 1] - 1, pieces), (int)(at % 32),
-                 [&](int w) { return shared_part(p, es, own_entries, w) + at % TR / 32; });
+                 [&](int w) { return shared_part(p, es, own_entries, w) + at % tr / 32; });
     }
-    join(w0, w1, n_, [&](int w) { return own_part(p, e, w) + blk; });
-    if (!valid)
+    if (valid)
+        join(w0, w1, n_, [&](int w) { return own_part(p, e, w) + blk; });
+    sm_ml[wave][lane] = f32x2{m, l};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sm_o[wave][i][lane] = o[i];
+    __syncthreads();
+    if (wave != 0 || !valid)
         return;
+#pragma unroll
+    for (int q = 1; q < JW; ++q) {
+        f32x4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = sm_o[q][i][lane];
+        add(sm_ml[q][lane], x);
+    }
     const int64_t t = first + row / p.G;
     const int hq = h * p.G + row % p.G;
     const float vs = E4M3 ? p.v_scale[h] : 1.0f;
@@ -269,29 +283,32 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(AttnParams p)
 namespace {
 
 struct Sizes {
+    int tile_rows;
     size_t own, shared; // entries
     int own_blocks;     // 32-row blocks of an own part
 };
 
-Sizes sizes_of(int B, int T, int K, int max_new, int H_kv, int G)
+Sizes sizes_of(int T, int B, int K, int max_new, int H_kv, int G, int d)
 {
     const int64_t rows = (int64_t)max_new * G;
-    return Sizes{((size_t)T * G / TR + B) * H_kv, ((size_t)T * G / TR + K) * H_kv,
-                 rows >= TR ? TR / 32 : (rows > 32 ? (int)((rows + 31) / 32) : 1)};
+    const int tr = d < 256 && rows <= kFewRows ? kFewRows : TR;
+    return Sizes{tr, ((size_t)T * G / tr + B) * H_kv, ((size_t)T * G / tr + K) * H_kv,
+                 rows >= tr ? tr / 32 : (rows > 32 ? (int)((rows + 31) / 32) : 1)};
 }
 
 } // namespace
 
 size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)
 {
-    const Sizes s = sizes_of(B, T, K, max_new, H_kv, G);
-    const int workgroups = (device_cus() + 7) / 8 * 8;
-    const size_t own = (s.own + workgroups) * s.own_blocks, blocks = own + (s.shared + workgroups) * NW;
+    const Sizes s = sizes_of(T, B, K, max_new, H_kv, G, d);
+    const int workgroups = (device_cus() + 7) / 8 * 8 * (TR / s.tile_rows);
+    const size_t own = (s.own + workgroups) * s.own_blocks, blocks = own + (s.shared + workgroups) * (s.tile_rows / 32);
     const size_t o = round256(blocks * 32 * d * 4), ml = round256(blocks * 32 * 2 * 4),
                  bf = round256((s.own + s.shared + 1) * 8), en = round256((s.own + s.shared) * kSharedEntry * 4);
     if (p) {
         char *at = static_cast<char *>(base);
         p->workgroups = workgroups;
+        p->tile_rows = s.tile_rows;
         p->own_blocks = s.own_blocks;
         p->shared_parts = (int64_t)own;
         p->part_o = reinterpret_cast<float *>(at);
@@ -306,18 +323,18 @@ size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int
 template <int D, bool E4M3>
 static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
 {
-    const Sizes s = sizes_of(p.B, p.T, p.K, p.max_new, p.H_kv, p.G);
+    const Sizes s = sizes_of(p.T, p.B, p.K, p.max_new, p.H_kv, p.G, D);
     AttnParams q = p;
-    q.block = block_keys(D);
+    q.block = block_keys(D, p.tile_rows == kFewRows);
     int own = (int)s.own, shared = (int)s.shared;
     void *plan[] = {&q, &own, &shared}, *args[] = {&q};
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_shared_plan_kernel), dim3(1), dim3(PT), plan, 0,
                                    stream);
     if (e == hipSuccess)
-        e = launch_attn_tiles_shared(p, D, E4M3, stream);
+        e = launch_attn_tiles_shared(q, D, E4M3, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_shared_join_kernel<D, E4M3>),
-                            dim3((unsigned)s.own, (unsigned)((s.own_blocks * (D / 32) + 3) / 4)), dim3(256), args, 0,
+                            dim3((unsigned)s.own, (unsigned)(s.own_blocks * (D / 32))), dim3(256), args, 0,
                             stream);
     return e;
 }

@@ -6,11 +6,10 @@
 
 namespace gdn {
 
-constexpr int TR = 256;  // rows of a tile
+// rows of a tile, and of one of a call with few rows a sequence (attn_shared.hip)
+constexpr int TR = 256, kFewRows = 128;
 // keys of a block: with 256 columns the queries take half of the LDS
-constexpr int block_keys(int d) { return d == 256 ? 32 : 128; }
-constexpr int NW = TR / 32; // waves
-constexpr int NT = 64 * NW;
+constexpr int block_keys(int d, bool few = false) { return d == 256 ? 32 : (few ? 64 : 128); }
 constexpr int PT = 1024; // the planning workgroup
 // what the plan says of an entry: kv head, tile, and its sequence, so that nobody reads the lengths again
 constexpr int kEntry = 8;
@@ -23,9 +22,9 @@ constexpr int kShared = 3;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s)
+__device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s, int tr = TR)
 {
-    return s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + TR - 1) / TR);
+    return s.kind == kSkip ? 0 : (int)(((int64_t)s.n * p.G + tr - 1) / tr);
 }
 
 // What a tile of a sequence sees: keys lo .. hi - 1, in blocks from lo on.
@@ -34,12 +33,12 @@ struct Span {
 };
 
 template <bool SHARED>
-__device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int tile)
+__device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int tile, int tr = TR)
 {
     Span x;
     const int rows = s.n * p.G;
-    const int last = (rows < (tile + 1) * TR ? rows : (tile + 1) * TR) - 1;
-    x.min_pos = s.L - s.n + tile * TR / p.G;
+    const int last = (rows < (tile + 1) * tr ? rows : (tile + 1) * tr) - 1;
+    x.min_pos = s.L - s.n + tile * tr / p.G;
     x.max_pos = s.L - s.n + last / p.G;
     x.hi = s.kind == kNormal && x.max_pos >= 0 ? x.max_pos + 1 : 0;
     x.lo = 0;
@@ -61,7 +60,7 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int t
 __device__ __forceinline__ int64_t own_part(const AttnParams &p, int e, int w) { return (int64_t)(e + w) * p.own_blocks; }
 __device__ __forceinline__ int64_t shared_part(const AttnParams &p, int e, int own_entries, int w)
 {
-    return p.shared_parts + (int64_t)(e - own_entries + w) * NW;
+    return p.shared_parts + (int64_t)(e - own_entries + w) * (p.tile_rows / 32);
 }
 
 // Exclusive sum over the planning workgroup.

@@ -170,15 +170,19 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
     }
 }
 
-// SHARED: of a plan with shared prefixes (attn_shared.hip).
-template <int D, bool E4M3, bool SHARED>
-__global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
+constexpr int waves_of(bool few) { return (few ? kFewRows : TR) / 32; }
+
+// SHARED: of a plan with shared prefixes (attn_shared.hip).  FEW: tiles of 128 rows, two workgroups a CU.
+template <int D, bool E4M3, bool SHARED, bool FEW = false>
+__global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnParams p)
 {
+    constexpr int TR = FEW ? kFewRows : gdn::TR;
+    constexpr int NW = waves_of(FEW), NT = 64 * NW;
     constexpr int CH = D / 8;                 // chunks of a row
     constexpr int ST = D / 16;                // steps of a score's contraction
     constexpr int DT = D / 32;                // 32-column tiles of o
     constexpr int ROWB = D * 2;               // bytes of an LDS row
-    constexpr int KB = block_keys(D);
+    constexpr int KB = block_keys(D, FEW);
     constexpr int SB = D == 256 ? 32 : 64;    // keys of a softmax step
     constexpr int NS = SB / 32;
     constexpr int KA = D == 256 ? 2 : 4; // products whose LDS reads go ahead together
@@ -228,7 +232,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
         const Seq s{uniform(entry[2]), uniform(entry[3]), uniform(entry[4]), uniform(entry[5]),
                     SHARED ? uniform(entry[7]) : 0, uniform(entry[6])};
         const long long t0 = p.before[e], t1 = p.before[e + 1];
-        const Span span = span_of<SHARED>(p, s, tile);
+        const Span span = span_of<SHARED>(p, s, tile, TR);
         const long long stop = t1 < u_end ? t1 : u_end;
         const int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
         const bool whole = u == t0 && stop == t1;
@@ -655,7 +659,7 @@ __global__ __launch_bounds__(NT, 2) void attn_tiles_kernel(AttnParams p)
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void attn_tiles_join_kernel(AttnParams p)
 {
-    constexpr int DT = D / 32, BATCH = 2;
+    constexpr int DT = D / 32, BATCH = 2, NW = waves_of(false);
     const int lane = threadIdx.x & 63, n_ = lane & 31, hh = lane >> 5;
     const int item = uniform(blockIdx.y * 4 + (threadIdx.x >> 6)), wave = item / DT, a = item % DT;
     // on the XCD that wrote it: some of it is still in its L2
@@ -750,30 +754,35 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
                                    stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, false>),
-                            dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
+                            dim3((unsigned)p.workgroups), dim3(64 * waves_of(false)), args, 0, stream);
     if (e == hipSuccess)
         e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_join_kernel<D, E4M3>),
-                            dim3((unsigned)p.workgroups, NW * (D / 32) / 4), dim3(256), args, 0, stream);
+                            dim3((unsigned)p.workgroups, waves_of(false) * (D / 32) / 4), dim3(256), args, 0, stream);
     return e;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool FEW>
 static hipError_t launch_shared(const AttnParams &p, hipStream_t stream)
 {
     AttnParams q = p;
-    q.block = block_keys(D);
     void *args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, true>),
-                           dim3((unsigned)p.workgroups), dim3(64 * NW), args, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, true, FEW>),
+                           dim3((unsigned)p.workgroups), dim3(64 * waves_of(FEW)), args, 0, stream);
 }
 
+// p.tile_rows: 256, or 128 with up to 128 columns
 hipError_t launch_attn_tiles_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
+    const bool few = p.tile_rows == kFewRows;
+    if (d == 64 && few)
+        return e4m3 ? launch_shared<64, true, true>(p, stream) : launch_shared<64, false, true>(p, stream);
     if (d == 64)
-        return e4m3 ? launch_shared<64, true>(p, stream) : launch_shared<64, false>(p, stream);
+        return e4m3 ? launch_shared<64, true, false>(p, stream) : launch_shared<64, false, false>(p, stream);
+    if (d == 128 && few)
+        return e4m3 ? launch_shared<128, true, true>(p, stream) : launch_shared<128, false, true>(p, stream);
     if (d == 128)
-        return e4m3 ? launch_shared<128, true>(p, stream) : launch_shared<128, false>(p, stream);
-    return e4m3 ? launch_shared<256, true>(p, stream) : launch_shared<256, false>(p, stream);
+        return e4m3 ? launch_shared<128, true, false>(p, stream) : launch_shared<128, false, false>(p, stream);
+    return e4m3 ? launch_shared<256, true, false>(p, stream) : launch_shared<256, false, false>(p, stream);
 }
 
 hipError_t launch_attn_tiles(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
