@@ -39,28 +39,30 @@ __device__ __forceinline__ int last_at(const int *first, int n, int v)
 
 } // namespace
 
+// One workgroup, as what it finds is one line; it waits for memory and for its own sums most of the time, so the first
+// PT sequences' numbers are read once, and a round's entries and the groups' are numbered together.
 __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int own_capacity, int shared_capacity)
 {
     __shared__ int g_begin[PT + 1], g_len[PT], g_low[PT], g_row[PT], g_members[PT], g_entry[PT], g_tiles[PT],
         g_first[PT], g_tokens[PT];
-    __shared__ int first_entry[PT + 1];
+    __shared__ int first_entry[PT], sm_cu[PT + 1];
     __shared__ Seq seqs[PT];
     const int tid = threadIdx.x;
-    // the first round's sequences, on their way while the groups are read
     Seq own{kSkip};
     if (tid < p.B)
         own = read_seq(p, tid);
-    if (tid < p.K) {
-        const int at = p.cu_groups[tid];
-        g_begin[tid] = at < 0 ? 0 : (at > p.B ? p.B : at);
-        g_len[tid] = p.shared_len[tid];
-        g_low[tid] = g_row[tid] = 0x7fffffff;
-        g_members[tid] = 0;
+    for (int x = tid; x <= PT && x <= p.B; x += PT)
+        sm_cu[x] = p.cu[x];
+    for (int x = tid; x <= p.K; x += PT) {
+        const int at = p.K > 0 ? p.cu_groups[x] : 0;
+        g_begin[x] = at < 0 ? 0 : (at > p.B ? p.B : at);
+        if (x < p.K) {
+            g_len[x] = p.shared_len[x];
+            g_low[x] = g_row[x] = 0x7fffffff;
+            g_members[x] = 0;
+        }
     }
-    if (tid == 0) {
-        const int at = p.cu_groups ? p.cu_groups[p.K] : 0;
-        g_begin[p.K] = at < 0 ? 0 : (at > p.B ? p.B : at);
-    }
+    seqs[tid] = own;
     __syncthreads();
     auto group_of = [&](int b) { // or -1
         if (p.K == 0)
@@ -68,9 +70,12 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         const int g = last_at(g_begin, p.K, b);
         return b >= g_begin[g] && b < g_begin[g + 1] ? g : -1;
     };
+    int own_group = -1;
     for (int b = tid; b < p.B; b += PT) {
         const Seq s = b == tid ? own : read_seq(p, b);
         const int g = s.kind == kNormal ? group_of(b) : -1;
+        if (b == tid)
+            own_group = g;
         if (g >= 0) {
             atomicMin(&g_len[g], s.L - s.n);
             atomicMin(&g_low[g], p.window > 0 ? s.L - s.n - p.window + 1 : 0);
@@ -79,102 +84,88 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         }
     }
     __syncthreads();
-    int mine = 0;
+    int group_entries = 0;
     if (tid < p.K) {
-        const int first = p.cu[g_begin[tid]], tokens = p.cu[g_begin[tid + 1]] - first;
+        const int x0 = g_begin[tid], x1 = g_begin[tid + 1], member = g_row[tid];
+        const int first = x0 <= PT ? sm_cu[x0] : p.cu[x0], tokens = (x1 <= PT ? sm_cu[x1] : p.cu[x1]) - first;
         const int len = g_len[tid] > 0 ? g_len[tid] & ~15 : 0, low = g_low[tid] > 0 ? g_low[tid] & ~15 : 0;
-        const bool ok = g_members[tid] > 1 && g_begin[tid] < g_begin[tid + 1] && len - low >= kLeastShared &&
-                        first >= 0 && tokens > 0 && first + tokens <= p.T;
+        const bool ok = g_members[tid] > 1 && x0 < x1 && len - low >= kLeastShared && first >= 0 && tokens > 0 &&
+                        first + tokens <= p.T;
         g_len[tid] = ok ? len : 0;
         g_low[tid] = low;
-        g_row[tid] = ok ? p.row[g_row[tid]] : 0;
+        g_row[tid] = ok ? (member < PT ? seqs[member].r : p.row[member]) : 0;
         g_first[tid] = first;
         g_tokens[tid] = tokens;
         g_tiles[tid] = ok ? (int)(((int64_t)tokens * p.G + p.tile_rows - 1) / p.tile_rows) : 0;
-        mine = g_tiles[tid] * p.H_kv;
+        group_entries = g_tiles[tid] * p.H_kv;
     }
-    // groups that overlap have more tiles than the workspace was sized for: what is past its end is left out
-    long long sum_groups;
-    const long long group_at = plan_scan((long long)mine, &sum_groups);
-    const int shared_entries = sum_groups < shared_capacity ? (int)sum_groups : shared_capacity;
-    if (tid < p.K)
-        g_entry[tid] = group_at < shared_entries ? (int)group_at : shared_entries;
-
-    // the sequences' own keys
-    int entries = 0;
+    int shared_entries = 0, entries = 0, own_entries = 0;
     long long units = 0;
     for (int b0 = 0; b0 < p.B; b0 += PT) {
         const int b = b0 + tid;
         int mine = 0;
-        __syncthreads(); // the round before has read the tables
+        __syncthreads(); // the round before has read the tables, and the groups are written
         if (b < p.B) {
             Seq s = b0 == 0 ? own : read_seq(p, b);
             mine = tiles_of(p, s, p.tile_rows) * p.H_kv;
-            const int g = s.kind == kNormal ? group_of(b) : -1;
+            const int g = b0 == 0 ? own_group : (s.kind == kNormal ? group_of(b) : -1);
             s.lo = g >= 0 && g_len[g] > 0 ? g + 1 : 0; // for now its group
             seqs[tid] = s;
         }
-        long long sum_all;
-        const long long mine_at = plan_scan((long long)mine, &sum_all);
+        // Sequences or groups that overlap have more tiles than the workspace was sized for (and than 32 bits
+        // count): what is past its end is left out.
+        long long sum_all, sum_groups;
+        long long group_at = group_entries; // of the first round
+        const long long mine_at = plan_scan2((long long)mine, &sum_all, &group_at, &sum_groups);
+        if (b0 == 0) {
+            shared_entries = sum_groups < shared_capacity ? (int)sum_groups : shared_capacity;
+            if (tid < p.K)
+                g_entry[tid] = group_at < shared_entries ? (int)group_at : shared_entries;
+        }
         const int room = own_capacity - entries, all = sum_all < room ? (int)sum_all : room;
         first_entry[tid] = mine_at < all ? (int)mine_at : all;
-        if (tid == 0)
-            first_entry[PT] = all;
         __syncthreads();
-        for (int e0 = 0; e0 < all; e0 += PT) {
+        const int seqs_here = p.B - b0 < PT ? p.B - b0 : PT;
+        const bool last_round = p.B - b0 <= PT;
+        own_entries = entries + all;
+        const int count = all + (last_round ? shared_entries : 0); // then the groups' common keys
+        for (int e0 = 0; e0 < count; e0 += PT) {
             const int e = e0 + tid;
             long long u = 0;
-            int h = 0, tile = 0, g = -1;
-            Seq s{};
+            i32x4 x0{0, 0, 0, 0}, x1 = x0, x2 = x0;
             if (e < all) {
-                const int q = last_at(first_entry, PT, e);
-                s = seqs[q];
-                g = s.lo - 1;
+                const int q = last_at(first_entry, seqs_here, e);
+                Seq s = seqs[q];
+                const int g = s.lo - 1;
                 s.lo = g >= 0 ? g_len[g] : 0;
-                const int tiles = tiles_of(p, s, p.tile_rows), x = e - first_entry[q];
-                h = x / tiles;
-                tile = x - h * tiles;
+                const int tiles = tiles_of(p, s, p.tile_rows), x = e - first_entry[q], h = x / tiles,
+                          tile = x - h * tiles;
                 u = span_of<true>(p, s, tile, p.tile_rows).blocks;
+                x0 = i32x4{h, tile, s.kind, s.first};
+                x1 = i32x4{s.n, s.L, s.r, s.lo};
+                if (g >= 0)
+                    x2 = i32x4{g_first[g], g_entry[g], g_tiles[g], 0};
+            } else if (e < count) {
+                const int g = last_at(g_entry, p.K, e - all);
+                const int x = e - all - g_entry[g], tiles = g_tiles[g] > 0 ? g_tiles[g] : 1, h = x / tiles;
+                u = (g_len[g] - g_low[g] + p.block - 1) / p.block;
+                x0 = i32x4{h, x - h * tiles, kShared, g_first[g]};
+                x1 = i32x4{g_tokens[g], g_len[g], g_row[g], g_low[g]};
             }
             long long sum;
             const long long at = units + plan_scan(u, &sum);
-            if (e < all) {
+            if (e < count) {
                 const int64_t o = entries + e;
                 p.before[o] = at;
                 i32x4 *to = reinterpret_cast<i32x4 *>(p.entry + o * kSharedEntry);
-                to[0] = i32x4{h, tile, s.kind, s.first};
-                to[1] = i32x4{s.n, s.L, s.r, s.lo};
-                to[2] = g >= 0 ? i32x4{g_first[g], g_entry[g], g_tiles[g], 0} : i32x4{0, 0, 0, 0};
+                to[0] = x0;
+                to[1] = x1;
+                to[2] = x2;
             }
             units += sum;
         }
-        entries += all;
+        entries += count;
     }
-    // the groups' common keys
-    const int own_entries = entries;
-    for (int e0 = 0; e0 < shared_entries; e0 += PT) {
-        const int e = e0 + tid;
-        long long u = 0;
-        int g = 0, h = 0, tile = 0;
-        if (e < shared_entries) {
-            g = last_at(g_entry, p.K, e);
-            const int x = e - g_entry[g], tiles = g_tiles[g] > 0 ? g_tiles[g] : 1;
-            h = x / tiles;
-            tile = x - h * tiles;
-            u = (g_len[g] - g_low[g] + p.block - 1) / p.block;
-        }
-        long long sum;
-        const long long at = units + plan_scan(u, &sum);
-        if (e < shared_entries) {
-            const int64_t o = entries + e;
-            p.before[o] = at;
-            i32x4 *to = reinterpret_cast<i32x4 *>(p.entry + o * kSharedEntry);
-            to[0] = i32x4{h, tile, kShared, g_first[g]};
-            to[1] = i32x4{g_tokens[g], g_len[g], g_row[g], g_low[g]};
-        }
-        units += sum;
-    }
-    entries += shared_entries;
     if (tid == 0) {
         p.before[entries] = units;
         p.count[0] = entries;

@@ -90,4 +90,39 @@ __device__ __forceinline__ T plan_scan(T v, T *total)
     return before + inc - v;
 }
 
+// Two of them at once; *b is its value and becomes its sum.
+__device__ __forceinline__ long long plan_scan2(long long a, long long *all_a, long long *b, long long *all_b)
+{
+    __shared__ long long wave_sum[2][PT / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    long long x = a, y = *b;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const long long o = __shfl_up(x, m), q = __shfl_up(y, m);
+        if (lane >= m) {
+            x += o;
+            y += q;
+        }
+    }
+    __syncthreads();
+    if (lane == 63) {
+        wave_sum[0][wave] = x;
+        wave_sum[1][wave] = y;
+    }
+    __syncthreads();
+    long long before_a = 0, before_b = 0;
+    *all_a = *all_b = 0;
+#pragma unroll
+    for (int w = 0; w < PT / 64; ++w) {
+        const long long o = wave_sum[0][w], q = wave_sum[1][w];
+        before_a += w < wave ? o : 0;
+        before_b += w < wave ? q : 0;
+        *all_a += o;
+        *all_b += q;
+    }
+    const long long at = before_a + x - a;
+    *b = before_b + y - *b;
+    return at;
+}
+
 } // namespace gdn
