@@ -44,6 +44,7 @@ struct AttnParams {
     const int32_t *cu_groups, *shared_len; // [K + 1], [K]
     int K;
     int tile_rows;              // rows of a tile
+    int pad;                    // units that an entry counts more than its blocks
     int own_blocks;             // 32-row blocks of a part of a sequence's own keys
     int64_t shared_parts;       // where the parts of shared keys begin, in 32-row blocks
 };

@@ -140,7 +140,7 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
                 s.lo = g >= 0 ? g_len[g] : 0;
                 const int tiles = tiles_of(p, s, p.tile_rows), x = e - first_entry[q], h = x / tiles,
                           tile = x - h * tiles;
-                u = span_of<true>(p, s, tile, p.tile_rows).blocks;
+                u = p.pad + span_of<true>(p, s, tile, p.tile_rows).blocks;
                 x0 = i32x4{h, tile, s.kind, s.first};
                 x1 = i32x4{s.n, s.L, s.r, s.lo};
                 if (g >= 0)
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
             } else if (e < count) {
                 const int g = last_at(g_entry, p.K, e - all);
                 const int x = e - all - g_entry[g], tiles = g_tiles[g] > 0 ? g_tiles[g] : 1, h = x / tiles;
-                u = (g_len[g] - g_low[g] + p.block - 1) / p.block;
+                u = p.pad + (g_len[g] - g_low[g] + p.block - 1) / p.block;
                 x0 = i32x4{h, x - h * tiles, kShared, g_first[g]};
                 x1 = i32x4{g_tokens[g], g_len[g], g_row[g], g_low[g]};
             }
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(AttnParams p)
         return;
     const long long total = *reinterpret_cast<const long long *>(p.count + 2);
     const int pieces = pieces_of(p, total);
-    const int w0 = owner_of(total, p.before[e], pieces), w1 = owner_of(total, p.before[e + 1] - 1, pieces);
+    const int w0 = owner_of(total, p.before[e] + p.pad, pieces), w1 = owner_of(total, p.before[e + 1] - 1, pieces);
     if (lo == 0 && w0 == w1)
         return; // whole, and it shares nothing: written by the tiles
     const int row = tile * tr + blk * 32 + n_;
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(AttnParams p)
         const int64_t at = (int64_t)(first - entry[8]) * p.G + row;
         const int es = own_entries + entry[9] + h * entry[10] + (int)(at / tr);
         if (es < p.count[0])
-            join(owner_of(total, p.before[es], pieces), owner_of(total, p.before[es + 1] - 1, pieces), (int)(at % 32),
+            join(owner_of(total, p.before[es] + p.pad, pieces), owner_of(total, p.before[es + 1] - 1, pieces), (int)(at % 32),
                  [&](int w) { return shared_part(p, es, own_entries, w) + at % tr / 32; });
     }
     if (valid)
@@ -317,6 +317,7 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     const Sizes s = sizes_of(p.T, p.B, p.K, p.max_new, p.H_kv, p.G, D);
     AttnParams q = p;
     q.block = block_keys(D, p.tile_rows == kFewRows);
+    q.pad = D == 256 ? 3 : 2;
     int own = (int)s.own, shared = (int)s.shared;
     void *plan[] = {&q, &own, &shared}, *args[] = {&q};
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&attn_shared_plan_kernel), dim3(1), dim3(PT), plan, 0,

@@ -234,8 +234,17 @@ __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnP
         const long long t0 = p.before[e], t1 = p.before[e + 1];
         const Span span = span_of<SHARED>(p, s, tile, TR);
         const long long stop = t1 < u_end ? t1 : u_end;
-        const int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
-        const bool whole = u == t0 && stop == t1;
+        int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
+        if constexpr (SHARED) { // an entry's first units are its beginning, which is the next piece's if this ends there
+            blk0 = blk0 > p.pad ? blk0 - p.pad : 0;
+            blk1 -= p.pad;
+            if (blk1 <= 0) {
+                u = stop;
+                ++e;
+                continue;
+            }
+        }
+        const bool whole = blk0 == 0 && stop == t1;
         const int slot = u == u_begin ? 0 : 1;
         if (!SHARED && tid == 0 && u == t0 && stop < t1)
             write_cut(p, w, Cut{owner_of(total, t1 - 1, pieces), slot, s.first, s.n * p.G, h, tile});
