@@ -67,7 +67,7 @@ def declare(L) -> None:
             ("attn_prologue", [_P] * 12, _i32),
             ("attn_paged", [_P, _P, _P, _P, _P, _P, _P, _f32, _P, size, _P], _i32),
             ("attn_paged_workspace_bytes", [_P], size),
-            ("attn_shared", [_P] * 7 + [_i32, _P, _P, _f32, _P, size, _P], _i32),
+            ("attn_shared", [_P] * 7 + [_i32, _i32, _P, _P, _f32, _P, size, _P], _i32),
             ("attn_shared_workspace_bytes", [_P, _i32], size),
             ("kv_page_workspace_bytes", [_i32, _i32, _i32], size),
             ("kv_page_reserve", [_P, _P, _P, _i32, _P, _P, size, _P], _i32),
@@ -334,13 +334,13 @@ def attn_shared_workspace_bytes(B: int, T: int, K: int, max_new: int, H_q: int, 
 
 
 def attn_shared(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, cu_groups, shared_len, out, workspace, *,
-                max_new: int, scale: float | None = None, window: int = 0, lse=None, k_scale=None, v_scale=None,
-                stream=None) -> None:
+                max_new: int, scale: float | None = None, window: int = 0, least: int | None = None, lse=None, k_scale=None,
+                v_scale=None, stream=None) -> None:
     """attn_paged for sequences that share prefixes, which are read once a group (see ``attn_shared`` in
     include/gdn.h).
 
     cu_groups [K+1] and shared_len [K] int32: sequences cu_groups[g] .. cu_groups[g+1]-1 have the same first
-    shared_len[g] positions; workspace a uint8 tensor of attn_shared_workspace_bytes; the rest as attn_paged."""
+    shared_len[g] positions, read together from `least` keys on (None: where it pays); workspace a uint8 tensor of attn_shared_workspace_bytes; the rest as attn_paged."""
     torch = _torch()
     bf, i32 = torch.bfloat16, torch.int32
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)
@@ -353,15 +353,18 @@ def attn_shared(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, cu_gro
     groups = shared_len.shape
     if len(groups) != 1 or cu_groups.shape != (groups[0] + 1,):
         raise ValueError("shared_len must be [K] and cu_groups [K+1]")
+    if least is not None and not 0 <= least < 1 << 31:
+        raise ValueError("least must be a number of keys")
     dev = _gpu(q, "q")
     _launch("attn_shared", lib().attn_shared, dev, stream,
             _DIMS.pack(B, T, R, H_q, H_kv, d, N, page, width, max_new, window, kind),
             _heads(q, "q", T, H_q, d, bf, dev),
             _cache(k_pages, v_pages, page_table, kv_len, k_scale, v_scale, dev, torch), _at(row, "row", i32, dev),
             _at(cu_seqlens, "cu_seqlens", i32, dev), _at(cu_groups, "cu_groups", i32, dev),
-            _at(shared_len, "shared_len", i32, dev), groups[0], _heads(out, "out", T, H_q, d, bf, dev),
-            _at_or_none(lse, "lse", torch.float32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
-            _at(workspace, "workspace", torch.uint8, dev), workspace.numel())
+            _at(shared_len, "shared_len", i32, dev), groups[0], -1 if least is None else least,
+            _heads(out, "out", T, H_q, d, bf, dev), _at_or_none(lse, "lse", torch.float32, dev),
+            1.0 / math.sqrt(d) if scale is None else scale, _at(workspace, "workspace", torch.uint8, dev),
+            workspace.numel())
 
 
 def kv_page_workspace_bytes(n: int, R: int, N: int) -> int:

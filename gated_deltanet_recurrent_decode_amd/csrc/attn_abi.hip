@@ -254,7 +254,7 @@ size_t attn_shared_workspace_bytes(const gdn_attn_dims *dims, int32_t groups)
 
 gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
                        const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
-                       const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
+                       int32_t least, const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
                        hipStream_t stream)
 {
     gdn::AttnParams p{};
@@ -272,6 +272,7 @@ gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_
     p.cu_groups = groups > 0 ? cu_groups : nullptr;
     p.shared_len = shared_len;
     p.K = groups;
+    p.least = least < 0 ? -1 : least;
     return from_hip(gdn::launch_attn_shared(p, dims->d, dims->cache_type == 1, stream));
 }
 

@@ -43,6 +43,7 @@ struct AttnParams {
     // a batch that shares prefixes
     const int32_t *cu_groups, *shared_len; // [K + 1], [K]
     int K;
+    int least;                  // keys from which a group is taken together; -1: by the plan's rule
     int tile_rows;              // rows of a tile
     int pad;                    // units that an entry counts more than its blocks
     int own_blocks;             // 32-row blocks of a part of a sequence's own keys

@@ -19,9 +19,17 @@ namespace gdn {
 
 namespace {
 
-// A group's keys are taken together from this many on: below, its rows' second parts cost more than the
-// keys that they read again.
-constexpr int kLeastShared = 128;
+// Which groups are taken together where the call does not say.  Members with tiles of their own read a key once a
+// tile; together they are `tiles` tiles, and `saved` fewer read it.  The rows' second parts have to be written and
+// joined for that, and the group's own tiles begun: about 4096 keys' time and 1024 more a tile.  16/2 heads of 128,
+// 512 rows, each row by itself / together, us: 64 groups of 8 with 1000 own keys at a prefix of 512 136 / 144, of 1024
+// 154 / 152, of 4096 273 / 191; 256 groups of 2 at 512 137 / 157, at 4096 299 / 312.  Chunks of 100-600 tokens fill
+// their own tiles: 499 / 509 with 12000 common keys.
+constexpr int kLeastSaved = 4096, kLeastSavedPerTile = 1024;
+// And the call as a whole saves at least so many blocks a workgroup: below, a step of few rows is bound by how long a
+// workgroup takes at all (64 rows of one group, 50 own keys, prefix 1024, 4 blocks: 26.3 / 27.3; 2048, 8: 31.2 / 29.5;
+// 8 rows at 4096: 27.6 / 28.2).
+constexpr int kLeastBlocks = 6;
 
 // The last x of n with first[x] <= v, the first at least.
 __device__ __forceinline__ int last_at(const int *first, int n, int v)
@@ -44,8 +52,9 @@ __device__ __forceinline__ int last_at(const int *first, int n, int v)
 __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int own_capacity, int shared_capacity)
 {
     __shared__ int g_begin[PT + 1], g_len[PT], g_low[PT], g_row[PT], g_members[PT], g_entry[PT], g_tiles[PT],
-        g_first[PT], g_tokens[PT];
+        g_first[PT], g_tokens[PT], g_own_tiles[PT];
     __shared__ int first_entry[PT], sm_cu[PT + 1];
+    __shared__ unsigned long long sm_saved; // blocks
     __shared__ Seq seqs[PT];
     const int tid = threadIdx.x;
     Seq own{kSkip};
@@ -59,10 +68,12 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
         if (x < p.K) {
             g_len[x] = p.shared_len[x];
             g_low[x] = g_row[x] = 0x7fffffff;
-            g_members[x] = 0;
+            g_members[x] = g_own_tiles[x] = 0;
         }
     }
     seqs[tid] = own;
+    if (tid == 0)
+        sm_saved = 0;
     __syncthreads();
     auto group_of = [&](int b) { // or -1
         if (p.K == 0)
@@ -81,22 +92,39 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
             atomicMin(&g_low[g], p.window > 0 ? s.L - s.n - p.window + 1 : 0);
             atomicMin(&g_row[g], b); // read through its first usable member
             atomicAdd(&g_members[g], 1);
+            atomicAdd(&g_own_tiles[g], tiles_of(p, s, p.tile_rows));
         }
     }
     __syncthreads();
-    int group_entries = 0;
+    int group_entries = 0, len = 0, low = 0, tokens = 0, first = 0, tiles = 0;
+    bool ok = false;
     if (tid < p.K) {
-        const int x0 = g_begin[tid], x1 = g_begin[tid + 1], member = g_row[tid];
-        const int first = x0 <= PT ? sm_cu[x0] : p.cu[x0], tokens = (x1 <= PT ? sm_cu[x1] : p.cu[x1]) - first;
-        const int len = g_len[tid] > 0 ? g_len[tid] & ~15 : 0, low = g_low[tid] > 0 ? g_low[tid] & ~15 : 0;
-        const bool ok = g_members[tid] > 1 && x0 < x1 && len - low >= kLeastShared && first >= 0 && tokens > 0 &&
-                        first + tokens <= p.T;
+        const int x0 = g_begin[tid], x1 = g_begin[tid + 1];
+        first = x0 <= PT ? sm_cu[x0] : p.cu[x0];
+        tokens = (x1 <= PT ? sm_cu[x1] : p.cu[x1]) - first;
+        len = g_len[tid] > 0 ? g_len[tid] & ~15 : 0;
+        low = g_low[tid] > 0 ? g_low[tid] & ~15 : 0;
+        tiles = (int)(((int64_t)tokens * p.G + p.tile_rows - 1) / p.tile_rows);
+        ok = g_members[tid] > 1 && x0 < x1 && len > low && first >= 0 && tokens > 0 && first + tokens <= p.T;
+        if (p.least >= 0) {
+            ok = ok && len - low >= p.least;
+        } else if (ok) {
+            const int64_t saved = (int64_t)(g_own_tiles[tid] - tiles) * (len - low);
+            ok = saved >= kLeastSaved + (int64_t)kLeastSavedPerTile * tiles;
+            if (ok)
+                atomicAdd(&sm_saved, (unsigned long long)(saved / p.block * p.H_kv));
+        }
+    }
+    __syncthreads();
+    if (tid < p.K) {
+        const int member = g_row[tid];
+        ok = ok && (p.least >= 0 || sm_saved >= (unsigned long long)kLeastBlocks * p.workgroups);
         g_len[tid] = ok ? len : 0;
         g_low[tid] = low;
         g_row[tid] = ok ? (member < PT ? seqs[member].r : p.row[member]) : 0;
         g_first[tid] = first;
         g_tokens[tid] = tokens;
-        g_tiles[tid] = ok ? (int)(((int64_t)tokens * p.G + p.tile_rows - 1) / p.tile_rows) : 0;
+        g_tiles[tid] = ok ? tiles : 0;
         group_entries = g_tiles[tid] * p.H_kv;
     }
     int shared_entries = 0, entries = 0, own_entries = 0;

@@ -515,12 +515,15 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * leaves them so): sequences cu_groups[g] .. cu_groups[g+1]-1 form group g of `groups`,
  * and the first shared_len[g] positions of its rows hold the same cells, whichever
  * pages they lie on; their keys are read once for the whole group, through the row of
- * its first usable sequence (the rest of each row through its own).  Every sequence's
+ * its first usable sequence (the rest of each row through its own).  least >= 0: groups
+ * with fewer common keys than that are read row by row; -1: those where the joining of
+ * the parts would cost more than it saves, by a rule on the lengths.  Every sequence's
  * result is that of attn_paged; its weights are rounded to bf16 at any max_new (o off by
  * 0.0023 of its norm).  A shared length that is longer than what a usable member has
  * before its new tokens counts as that, a negative one as 0; a sequence may be in no
  * group.  A row that reads the common positions through a page outside [1, N) gets
- * NaN in o and lse; the other members' entries for them are not looked at.
+ * NaN in o and lse; the other members' entries for them are not looked at where the
+ * group is read together.
  * cu_groups [groups + 1] and shared_len [groups] int32 on the device (NULL with groups
  * 0); 0 <= groups <= 1024.  Preconditions, not checked: cu_groups is non-decreasing in
  * [0, B]; the common cells agree.  workspace: attn_shared_workspace_bytes(dims, groups)
@@ -528,7 +531,7 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  */
 gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
                        const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
-                       const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
+                       int32_t least, const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
 /* The workspace attn_shared needs for dims (B, T, max_new, H_q, H_kv, d) and groups; 0

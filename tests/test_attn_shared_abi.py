@@ -29,7 +29,7 @@ def shared(d=None, q=None, c=None, row=FAKE, cu=FAKE, groups=FAKE, lens=FAKE, K=
     d = dims() if d is None else d
     c = at.KvCache(FAKE, FAKE, None, None, FAKE, FAKE) if c is None else c
     return gdn.lib().attn_shared(None if no_dims else ctypes.byref(d), ctypes.byref(q or heads()), ctypes.byref(c), row,
-                                 cu, groups, lens, K, ctypes.byref(out or heads()), None, scale, ws, nbytes, None)
+                                 cu, groups, lens, K, -1, ctypes.byref(out or heads()), None, scale, ws, nbytes, None)
 
 
 def test_refusals():
@@ -63,7 +63,7 @@ def test_layout_checks():
                 page_table=meta(5, 8), kv_len=meta(5), row=meta(2), cu_seqlens=meta(3), cu_groups=meta(2),
                 shared_len=meta(1), out=meta(4, 4, 64, dtype=bf), workspace=meta(1, dtype=torch.uint8), max_new=2)
     for name, bad, why in (("cu_groups", meta(3), "cu_groups"), ("shared_len", meta(1, 1), "shared_len"),
-                           ("page_table", None, "page_table"), ("lse", meta(4), "lse"), ("row", meta(3), "row must be")):
+                           ("page_table", None, "page_table"), ("lse", meta(4), "lse"), ("least", -1, "least"), ("least", 1 << 31, "least"), ("row", meta(3), "row must be")):
         with pytest.raises(ValueError, match=why):
             gdn.attn_shared(**{**good, name: bad})
     with pytest.raises(ValueError, match="GPU tensor"):

@@ -39,7 +39,7 @@ class Forked(H.Cache):
         return int(self.table[int(self.row[b])][t // self.page]), t % self.page
 
 
-def run(c, *, window=0, groups=None, shared=None, max_new=None, call=None, **over):
+def run(c, *, window=0, groups=None, shared=None, max_new=None, least=16, **over):
     t = c.cuda(**over)
     K = len(c.groups) - 1 if groups is None else len(groups) - 1
     out = torch.full((c.T, c.H_q, c.d), 7.0, dtype=H.BF, device="cuda")
@@ -49,7 +49,8 @@ def run(c, *, window=0, groups=None, shared=None, max_new=None, call=None, **ove
                     dtype=torch.uint8, device="cuda")
     gdn.attn_shared(c.q.cuda(), t.pop("k_pages"), t.pop("v_pages"), t.pop("page_table"), t.pop("kv_len"),
                     t.pop("row"), t.pop("cu_seqlens"), i32(c.groups if groups is None else groups),
-                    i32(c.shared if shared is None else shared), out, ws, max_new=max_new, window=window, lse=lse, **t)
+                    i32(c.shared if shared is None else shared), out, ws, max_new=max_new, window=window,
+                    least=least, lse=lse, **t)
     torch.cuda.synchronize()
     return out, lse
 
@@ -200,7 +201,7 @@ def test_captured_and_replayed_with_other_lengths_on_another_stream():
 
     def call():
         gdn.attn_shared(q, t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"], t["row"], t["cu_seqlens"], groups,
-                        shared, out, ws, max_new=2)
+                        shared, out, ws, max_new=2, least=16)
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -223,6 +224,24 @@ def test_captured_and_replayed_with_other_lengths_on_another_stream():
         H.check(out, o, tol, f"o of the replay at {cutoff}, {own}")
 
 
+def test_which_groups_are_read_together():
+    # a group that is read together is read through its first member's row: the other rows' entries for the common
+    # keys may then name no page at all
+    c = Forked([(2048, [(1, i % 40) for i in range(64)]), (48, [(1, 5), (1, 9)])], H_q=4, H_kv=2, d=64, page=64, seed=13)
+    table = c.table.clone()
+    for i in range(1, 64):
+        table[int(c.row[i]), :2048 // 64] = 0
+    o, l, tol, tol_l = H.attention(c, c.d ** -0.5)
+    for least in (None, 2048, 100):
+        out, lse = run(c, least=least, page_table=table.cuda())
+        H.check(out, o, tol, f"o from {least} keys on")
+        H.check(lse, l, tol_l, f"lse from {least} keys on")
+    out, lse = run(c, least=2049, page_table=table.cuda())
+    assert bool(out[1:64].isnan().all()) and bool(lse[1:64].isnan().all())
+    H.check(out[[0, 64, 65]], o[[0, 64, 65]], tol[[0, 64, 65]], "o of the rows with pages")
+    check(c, *run(c, least=None, shared=[100, 48]))  # too little to save
+
+
 def test_strided_heads():
     c = Forked([(300, [(1, 5), (3, 60)])], H_q=4, H_kv=2, d=64, page=16, seed=12)
     t = c.cuda()
@@ -232,7 +251,7 @@ def test_strided_heads():
     wide = torch.full((c.T, 8, 64), 7.0, dtype=H.BF, device="cuda")
     ws = torch.empty(gdn.attn_shared_workspace_bytes(c.B, c.T, 1, 3, 4, 2, 64), dtype=torch.uint8, device="cuda")
     gdn.attn_shared(q, t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"], t["row"], t["cu_seqlens"],
-                    i32(c.groups), i32(c.shared), wide[:, ::2], ws, max_new=3)
+                    i32(c.groups), i32(c.shared), wide[:, ::2], ws, max_new=3, least=16)
     torch.cuda.synchronize()
     o, _, tol, _ = H.attention(c, 0.125)
     H.check(wide[:, ::2], o, tol, "o")
