@@ -20,16 +20,16 @@ namespace gdn {
 namespace {
 
 // Which groups are taken together where the call does not say.  Members with tiles of their own read a key once a
-// tile; together they are `tiles` tiles, and `saved` fewer read it.  The rows' second parts have to be written and
-// joined for that, and the group's own tiles begun: about 4096 keys' time and 1024 more a tile.  16/2 heads of 128,
-// 512 rows, each row by itself / together, us: 64 groups of 8 with 1000 own keys at a prefix of 512 136 / 144, of 1024
-// 154 / 152, of 4096 273 / 191; 256 groups of 2 at 512 137 / 157, at 4096 299 / 312.  Chunks of 100-600 tokens fill
-// their own tiles: 499 / 509 with 12000 common keys.
-constexpr int kLeastSaved = 4096, kLeastSavedPerTile = 1024;
+// tile; together they are fewer tiles.  For that the rows' second parts have to be written and joined, about 512 keys'
+// time for a tile of a member, and the group's own tiles begun, 1024 each.  16/2 heads of 128, 512 rows with 10-2000 own
+// keys, each row by itself / together, us: 256 groups of about 2 at a prefix of 1024 182 / 180, of 2048 244 / 224, of
+// 8192 622 / 491; 64 groups of about 8 at 512 139 / 148, of 1024 155 / 153, of 4096 313 / 191.  Chunks of 100-600
+// tokens fill their own tiles: 499 / 509 with 12000 common keys.
+constexpr int kPerMember = 512, kPerTile = 1024;
 // And the call as a whole saves at least so many blocks a workgroup: below, a step of few rows is bound by how long a
-// workgroup takes at all (64 rows of one group, 50 own keys, prefix 1024, 4 blocks: 26.3 / 27.3; 2048, 8: 31.2 / 29.5;
-// 8 rows at 4096: 27.6 / 28.2).
-constexpr int kLeastBlocks = 6;
+// workgroup takes at all (64 rows in 16 groups at 1024, 3 blocks: 33.5 / 33.3; at 2048, 6: 41.6 / 37.6; 8 rows of one
+// group at 4096, 2: 27.9 / 28.7; 64 rows of one at 1024, 4: 26.8 / 27.9).
+constexpr int kLeastBlocks = 5;
 
 // The last x of n with first[x] <= v, the first at least.
 __device__ __forceinline__ int last_at(const int *first, int n, int v)
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
             ok = ok && len - low >= p.least;
         } else if (ok) {
             const int64_t saved = (int64_t)(g_own_tiles[tid] - tiles) * (len - low);
-            ok = saved >= kLeastSaved + (int64_t)kLeastSavedPerTile * tiles;
+            ok = saved >= (int64_t)kPerMember * g_own_tiles[tid] + (int64_t)kPerTile * tiles;
             if (ok)
                 atomicAdd(&sm_saved, (unsigned long long)(saved / p.block * p.H_kv));
         }
