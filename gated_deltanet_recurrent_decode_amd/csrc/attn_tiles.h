@@ -57,7 +57,10 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, const Seq &s, int t
 
 // The place of a part of entry e of a plan with shared prefixes, in 32-row blocks: walking along the line, every
 // new (entry, piece) is another entry or another piece, so their sum numbers them.
-__device__ __forceinline__ int64_t own_part(const AttnParams &p, int e, int w) { return (int64_t)(e + w) * p.own_blocks; }
+__device__ __forceinline__ int64_t own_part(const AttnParams &p, int e, int w)
+{
+    return (int64_t)(e + w) * p.own_blocks;
+}
 __device__ __forceinline__ int64_t shared_part(const AttnParams &p, int e, int own_entries, int w)
 {
     return p.shared_parts + (int64_t)(e - own_entries + w) * (p.tile_rows / 32);

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnP
         const Span span = span_of<SHARED>(p, s, tile, TR);
         const long long stop = t1 < u_end ? t1 : u_end;
         int blk0 = (int)(u - t0), blk1 = (int)(stop - t0);
-        if constexpr (SHARED) { // an entry's first units are its beginning, which is the next piece's if this ends there
+        if constexpr (SHARED) { // its first units are its beginning, which is the next piece's if this one ends there
             blk0 = blk0 > p.pad ? blk0 - p.pad : 0;
             blk1 -= p.pad;
             if (blk1 <= 0) {

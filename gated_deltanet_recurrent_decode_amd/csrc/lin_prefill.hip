@@ -17,6 +17,18 @@
 // A long prompt has more tokens than one workgroup should walk: it is cut into segments.  A first kernel
 // forms each segment's own part of the state, a second carries them on along the prompt, and the walk then
 // begins every segment with its state.
+//
+// What bounds it: memory, with what the segments add to it.  8191 tokens at 16 heads of 128 x 128 have to move 135 MB
+// (26 us at a large copy's 5.2 TB/s) and move 334, k and v twice and the segments' states four times; own parts 25 us,
+// carry 12, walk 40, calls back to back 74 to 76; without any of its products the walk is 10% faster.  16 prompts of
+// 100-1500 tokens 124 us, 4 of 5000-9000 with four value heads of 64 columns a key head 202 to 204, one of 77 10.4.
+//
+// Scores and scales are dealt out among a head's waves (each forming all for itself: 89 -> 81 us, the long
+// prompt's call); two barriers a chunk with 48 KiB of LDS less (81 -> 76).  Two value heads of a key head in one
+// workgroup where they have 64 columns: q and k are read once for both (4 prompts 243 -> 205).  Tried and not faster,
+// the long prompt's call: 64 or 16 columns a wave, rings of three and four chunks, stores of o past the cache (76 ->
+// 81), two accumulators of a read-out, three waves a SIMD, the state's second number left out of the read-outs (4 to
+// 8% of the time for half of its bits).
 
 #include <type_traits>
 
@@ -424,8 +436,8 @@ __global__ __launch_bounds__(HPW *DV * 2, 2) void lin_prefill_kernel(LinPrefillP
         bring(0, 0);
     if constexpr (OUT) // scores of later keys: stay 0
         for (int x = tid; x < HPW * 2 * 16 * 4; x += NT)
-            *reinterpret_cast<u32x2 *>(&sm_p[x >> 7][x >> 6 & 1][score_at(x >> 2 & 15, 2 + (x >> 1 & 1)) + (x & 1) * 8]) =
-                u32x2{0u, 0u};
+            *reinterpret_cast<u32x2 *>(
+                &sm_p[x >> 7][x >> 6 & 1][score_at(x >> 2 & 15, 2 + (x >> 1 & 1)) + (x & 1) * 8]) = u32x2{0u, 0u};
     // S is there: left to the compiler, every chunk would wait for it, and with it for what is asked for meanwhile
 #pragma unroll
     for (int t = 0; t < TK; ++t)
@@ -644,7 +656,9 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
 {
     // Tokens of a segment: the shortest ones that give at most `rounds` times the workgroups that the chip holds
     // at once, sequences' last ones counted as whole, with the rounds that cost least.  A workgroup's start and end
-    // and its state's way through memory cost about as much as kFixed tokens.
+    // and its state's way through memory cost about as much as kFixed tokens: segments half as long
+    // take 77, 146 and 223 us of the three cases above, twice as long 78, 123 and 335, these 76, 126 and 205.  kMost: where no rounds fit (thousands of sequences), and none
+    // longer, so that one long prompt among them does not outlast the rest.
     constexpr int64_t kFixed = 160, kMost = 2048;
     const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
     const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);

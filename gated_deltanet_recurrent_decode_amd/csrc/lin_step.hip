@@ -5,7 +5,9 @@
 // values of q and k are 16-byte loads and the read-out's sum over the rows ends inside the wave (in the
 // thread, then over lane bits 3 to 5).
 //
-// What bounds it: the state, read once and written once.
+// What bounds it: the state, read once and written once.  MI355X, calls back to back: 64 rows at 16 heads of 128 x 128
+// 26.4 us (5.1 TB/s, as a large copy), 24 rows of 4 tokens at 32 heads of 128 x 64 with all states kept 24.0 (5.3
+// TB/s); one row 4.5 us of a kernel, what a launch costs.
 
 #include "attn_common.h"
 #include "lin_internal.h"

@@ -678,7 +678,9 @@ gdn_status lin_attn_step_tokens(const gdn_lin_dims *dims, const gdn_heads *q, co
  * Sums, states and decays are fp32 (a chunk's sums of log decays 64 bits).  For the
  * matrix cores, decayed values go into the state as three bf16 numbers, with all their
  * bits; the state and the weights that make a read-out go as two, off by at most
- * 2^-15 of themselves, before o is rounded once, to bf16.
+ * 2^-15 of themselves, before o is rounded once, to bf16.  Within a call a state is held
+ * at up to 2^64 times its value: entries of v or of the state of 2^63 (9e18) and more
+ * may come out as infinities.
  * Results match lin_attn_step within rounding, not bit for bit, and the same call gives
  * the same bits again.  An infinity or NaN in a token shows from that token on, as an
  * infinity or NaN, and nowhere before.
