@@ -12,19 +12,19 @@
 // member has before its new tokens, and to whole 16 keys (a block's staging rows lie on one page so).  Longer or
 // shorter, the result is the same; only what is read once changes.
 //
-// What bounds it, with few rows: a wave's own chain through a block (scores, maximum, weights, products: 1.05 us for 64
-// keys, which take the matrix cores 0.4), hidden by one other wave of its SIMD at most, for a tile's registers allow
-// two; an entry's beginning (its record, its page numbers and its first block behind each other, 2.5 us); the plan and
-// the join, 8.5 and 5 to 11 us of a call.  With many rows a sequence: the matrix cores, as in attn_tiles.hip.
+// What bounds it, with few rows: a wave's own chain through a block (scores, maximum, weights, products: 1.05 us for
+// 64 keys, which take the matrix cores 0.4), hidden by one other wave of its SIMD at most, for a tile's registers
+// allow two; an entry's beginning (its record, its page numbers and its first block behind each other, 2.5 us); the
+// plan and the join, 8.5 and 5 to 11 us of a call.  With many rows a sequence: the matrix cores, as in attn_tiles.hip.
 // MI355X, calls back to back: 64 rows at 32/4 heads of 128 over a prefix of 8000 and 50-800 own keys 45 to 47 us (each
 // row by itself 139); 48 rows in 3 groups at 32/8 heads of 128, e4m3, 4000-30000 and 100-1000 86 us (355); 32 rows of 4
 // tokens at 16/4 heads of 256 over 6001 and 10-500 60 us (126); 8 chunks of 100-600 tokens at 32/4 heads of 128 over
 // 12000 492 to 515 us (967 to 924 TFLOP/s), where the rule below takes nothing together.
 //
-// Tried, calls unless said: a tile's keys dealt out among its idle waves (the same); the waves' page numbers a block of
-// 64 ahead in a register (the same); own keys by a kernel of 16-row tiles beside the groups' tiles, one more launch (8
-// rows 30 -> 36 us, 64 rows 62 -> 66, 3 groups 123 -> 111, all before the tiles of 128 rows); a block's weight on the
-// line by the waves that have rows (3 groups 86.6 -> 85.1, 64 rows 47.0 -> 49.8, chunks 503 -> 535).
+// Tried, calls: a tile's keys dealt out among its idle waves (the same); the waves' page numbers a block of 64 ahead
+// in a register (the same); own keys by a kernel of 16-row tiles beside the groups' tiles, one more launch (8 rows 30
+// -> 36 us, 64 rows 62 -> 66, 3 groups 123 -> 111, all before the tiles of 128 rows); a block's weight on the line by
+// the waves that have rows (3 groups 86.6 -> 85.1, 64 rows 47.0 -> 49.8, chunks 503 -> 535).
 
 #include "attn_tiles.h"
 #include "gdn_internal.h"
@@ -330,103 +330,6 @@ Sizes sizes_of(int T, int B, int K, int max_new, int H_kv, int G, int d)
     // 128 53.7 / 51.1, 256 71.8 / 72.9, 2048 380 / 403.  Tiles of 64, four a CU, read a group's keys twice as often and
     // leave twice the parts (64 rows 57 -> 59, 3 groups 99 -> 93, before an entry's beginning was counted).  With 256
     // columns the LDS has no room for two.
-    const int tr = p.tile_rows;
-    if (kind != kNormal || tile * tr + blk * 32 >= rows)
-        return;
-    const long long total = *reinterpret_cast<const long long *>(p.count + 2);
-    const int pieces = pieces_of(p, total);
-    const int w0 = owner_of(total, p.before[e] + p.pad, pieces), w1 = owner_of(total, p.before[e + 1] - 1, pieces);
-    if (lo == 0 && w0 == w1)
-        return; // whole, and it shares nothing: written by the tiles
-    const int row = tile * tr + blk * 32 + n_;
-    const bool valid = row < rows;
-    float m = neg_inf(), l = 0.f;
-    f32x4 o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto add = [&](f32x2 ml, const f32x4(&x)[4]) {
-        const float top = fmaxf(m, ml[0]), safe = top == neg_inf() ? 0.f : top;
-        const float keep = __builtin_amdgcn_exp2f(m - safe), f = __builtin_amdgcn_exp2f(ml[0] - safe);
-        l = fmaf(ml[1], f, l * keep);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            o[i >> 2][i & 3] = fmaf(x[i >> 2][i & 3], f, o[i >> 2][i & 3] * keep);
-        m = top;
-    };
-    // this wave's of the parts w_a .. w_b of a row: at(w) their 32-row block, r the row in it
-    auto join = [&](int w_a, int w_b, int r, auto at) {
-        constexpr int BATCH = 2;
-        for (int w = w_a + wave; w <= w_b; w += JW * BATCH) {
-            f32x2 ml[BATCH];
-            f32x4 po[BATCH][4];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int64_t part = at(w + k * JW <= w_b ? w + k * JW : w);
-                ml[k] = *reinterpret_cast<const f32x2 *>(p.part_ml + (part * 32 + r) * 2);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    po[k][i] = *reinterpret_cast<const f32x4 *>(p.part_o + part * 32 * D + a * 1024 + i * 256 +
-                                                                (hh * 32 + r) * 4);
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                if (w + k * JW <= w_b)
-                    add(ml[k], po[k]);
-        }
-    };
-    if (lo > 0 && valid) { // the row's place among its group's
-        const int64_t at = (int64_t)(first - entry[8]) * p.G + row;
-        const int es = own_entries + entry[9] + h * entry[10] + (int)(at / tr);
-        if (es < p.count[0])
-            join(owner_of(total, p.before[es] + p.pad, pieces), owner_of(total, p.before[es + 1] - 1, pieces),
-                 (int)(at % 32), [&](int w) { return shared_part(p, es, own_entries, w) + at % tr / 32; });
-    }
-    if (valid)
-        join(w0, w1, n_, [&](int w) { return own_part(p, e, w) + blk; });
-    sm_ml[wave][lane] = f32x2{m, l};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sm_o[wave][i][lane] = o[i];
-    __syncthreads();
-    if (wave != 0 || !valid)
-        return;
-#pragma unroll
-    for (int q = 1; q < JW; ++q) {
-        f32x4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = sm_o[q][i][lane];
-        add(sm_ml[q][lane], x);
-    }
-    const int64_t t = first + row / p.G;
-    const int hq = h * p.G + row % p.G;
-    const float vs = E4M3 ? p.v_scale[h] : 1.0f;
-    const float inv = l == 0.f ? 0.f : vs / l;
-    uint16_t *out = p.out.p + t * p.out.row + (int64_t)hq * p.out.head + a * 32 + 4 * hh;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2 *>(out + 8 * i) =
-            u32x2{pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv)};
-    if (a == 0 && hh == 0 && p.lse)
-        p.lse[t * p.H_q + hq] = lse_of(m, l);
-}
-
-namespace {
-
-struct Sizes {
-    int tile_rows;
-    size_t own, shared; // entries
-    int own_blocks;     // 32-row blocks of an own part
-};
-
-Sizes sizes_of(int T, int B, int K, int max_new, int H_kv, int G, int d)
-{
-    const int64_t rows = (int64_t)max_new * G;
-    // Few rows a sequence leave most waves of a 256-row tile idle: then tiles of 128 with blocks of 64 keys, so that a CU
-    // holds two workgroups and one's waits are the other's work (3 groups 128 -> 99 us, 64 rows 64 -> 57; tiles of 64, four
-    // a CU, read a group's keys twice as often and leave twice the parts: 93 and 59).  With 256 columns the LDS has no
-    // room for two.
     const int tr = d < 256 && rows <= kFewRows ? kFewRows : TR;
     return Sizes{tr, ((size_t)T * G / tr + B) * H_kv, ((size_t)T * G / tr + K) * H_kv,
                  rows >= tr ? tr / 32 : (rows > 32 ? (int)((rows + 31) / 32) : 1)};

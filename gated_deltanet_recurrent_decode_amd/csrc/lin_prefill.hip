@@ -656,9 +656,9 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
 {
     // Tokens of a segment: the shortest ones that give at most `rounds` times the workgroups that the chip holds
     // at once, sequences' last ones counted as whole, with the rounds that cost least.  A workgroup's start and end
-    // and its state's way through memory cost about as much as kFixed tokens: segments half as long
-    // take 77, 146 and 223 us of the three cases above, twice as long 78, 123 and 335, these 76, 126 and 205.  kMost: where no rounds fit (thousands of sequences), and none
-    // longer, so that one long prompt among them does not outlast the rest.
+    // and its state's way through memory cost about as much as kFixed tokens: segments half as long take 77, 146 and
+    // 223 us of the three cases above, twice as long 78, 123 and 335, these 76, 126 and 205.  kMost: where no rounds
+    // fit (thousands of sequences), and none longer, so that one long prompt among them does not outlast the rest.
     constexpr int64_t kFixed = 160, kMost = 2048;
     const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
     const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);
