@@ -266,7 +266,8 @@ gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_
         return GDN_ERR_SHAPE;
     if (groups > 0 && (!cu_groups || !shared_len))
         return GDN_ERR_NULL;
-    if (((int64_t)p.T * p.G / 256 + groups) * p.H_kv > INT32_MAX / 4 ||
+    // the join's grid: an entry is 256 threads of 2^32
+    if (((int64_t)p.T * p.G / 128 + (p.B > groups ? p.B : groups)) * p.H_kv >= 1 << 24 ||
         workspace_bytes < gdn::attn_shared_layout(p.B, p.T, groups, p.max_new, p.H_kv, p.G, dims->d, workspace, &p))
         return GDN_ERR_SHAPE;
     p.cu_groups = groups > 0 ? cu_groups : nullptr;

@@ -151,7 +151,9 @@ __global__ __launch_bounds__(PT) void attn_shared_plan_kernel(AttnParams p, int 
             Seq s = b0 == 0 ? own : read_seq(p, b);
             mine = tiles_of(p, s, p.tile_rows) * p.H_kv;
             const int g = b0 == 0 ? own_group : (s.kind == kNormal ? group_of(b) : -1);
-            s.lo = g >= 0 && g_len[g] > 0 ? g + 1 : 0; // for now its group
+            // For now its group.  Its tokens are among the group's if cu_seqlens does not decrease; the join relies on it.
+            s.lo = g >= 0 && g_len[g] > 0 && s.first >= g_first[g] && s.first + s.n <= g_first[g] + g_tokens[g] ? g + 1
+                                                                                                               : 0;
             seqs[tid] = s;
         }
         // Sequences or groups that overlap have more tiles than the workspace was sized for (and than 32 bits

@@ -142,7 +142,7 @@ gdn_status lin_attn_prefill(const gdn_lin_dims *dims, const gdn_heads *q, const 
         return GDN_ERR_UNSUPPORTED;
     gdn::LinPrefillParams p{};
     if (workspace_bytes < gdn::lin_prefill_layout(d.B, d.T, d.H_k, d.H_v, d.d_k, d.d_v, workspace, &p) ||
-        (int64_t)p.segments * d.H_v >= 1 << 24)
+        (int64_t)p.segments * d.H_v >= 1 << 23) // 256 threads each, rounded up, of 2^32
         return GDN_ERR_SHAPE;
     p.q = heads_of(*q);
     p.k = heads_of(*k);

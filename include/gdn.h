@@ -527,7 +527,8 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * cu_groups [groups + 1] and shared_len [groups] int32 on the device (NULL with groups
  * 0); 0 <= groups <= 1024.  Preconditions, not checked: cu_groups is non-decreasing in
  * [0, B]; the common cells agree.  workspace: attn_shared_workspace_bytes(dims, groups)
- * bytes.  The rest, and statuses, as attn_paged (GDN_ERR_SHAPE also for groups).
+ * bytes.  The rest, and statuses, as attn_paged (GDN_ERR_SHAPE also for groups, and where
+ * (T H_q / H_kv / 128 + B) H_kv is 2^24 or more).
  */
 gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
                        const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,

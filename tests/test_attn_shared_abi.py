@@ -41,6 +41,8 @@ def test_refusals():
         assert shared(**bad) == NULL, bad
     for bad in (dict(B=-1), dict(R=0), dict(H_q=5), dict(max_new=-1), dict(window=-1), dict(T=1 << 30)):
         assert shared(dims(**bad)) == SHAPE, bad
+    for bad in (dict(B=1 << 23), dict(T=1 << 26, H_q=16, H_kv=16, max_new=1 << 20), dict(B=1 << 20, H_q=32, H_kv=16)):
+        assert shared(dims(**bad)) == SHAPE, bad  # more entries than the join's grid counts
     for bad in (dict(d=96), dict(page_size=8), dict(cache_type=2)):
         assert shared(dims(**bad)) == UNSUPPORTED, bad
     assert shared(K=-1) == SHAPE and shared(K=1025) == SHAPE and shared(scale=math.nan) == SHAPE

@@ -242,6 +242,15 @@ def test_which_groups_are_read_together():
     check(c, *run(c, least=None, shared=[100, 48]))  # too little to save
 
 
+def test_ranges_that_go_back():
+    # the third sequence's tokens lie before the first's: its row by itself, and nobody's parts
+    c = Forked([(640, [(2, 5), (2, 9), (2, 3), (2, 4)])], H_q=4, H_kv=2, d=64, page=16, seed=14)
+    out, lse = run(c, cu_seqlens=torch.tensor([3, 5, 1, 3, 5], dtype=torch.int32))
+    c.cu = torch.tensor([1, 1, 1, 3, 3], dtype=torch.int32)
+    check(c, out, lse, tokens=slice(1, 3))
+    assert bool((out[[0, 5, 6, 7]] == 7).all()) and bool((lse[[0, 5, 6, 7]] == 7).all())
+
+
 def test_strided_heads():
     c = Forked([(300, [(1, 5), (3, 60)])], H_q=4, H_kv=2, d=64, page=16, seed=12)
     t = c.cuda()

@@ -60,6 +60,7 @@ def test_refusals(name):
 
 
 def test_refusals_of_one_call():
+    assert call("lin_attn_prefill", dims(T=(1 << 30) - 1, H_k=16, H_v=16)) == SHAPE  # segments of 16 heads
     assert call("lin_attn_step", dims(T=0)) == SHAPE and call("lin_attn_step", dims(B=1 << 10, T=1 << 20)) == SHAPE
     assert call("lin_attn_step_tokens", slots=None) == NULL
     assert call("lin_attn_prefill", cu=None) == NULL and call("lin_attn_prefill", ws=None) == NULL
