@@ -67,6 +67,8 @@ hipError_t launch_attn_prologue(const AttnPrologueParams &p, int d, bool e4m3, h
 // device scratch in bytes; fills the parameter block's pointers when it is given
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p);
+// whether attn_paged takes its 16-row tiles
+bool attn_few_rows(int max_new, int G);
 size_t attn_rows_layout(int d, void *base, AttnParams *p);
 size_t attn_tiles_layout(int B, int T, int H_kv, int G, int d, void *base, AttnParams *p);
 hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t stream);

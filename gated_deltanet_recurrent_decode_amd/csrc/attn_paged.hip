@@ -667,17 +667,18 @@ hipError_t launch_attn_rows(const AttnParams &p, int d, bool e4m3, hipStream_t s
 // and 50 / 38 at the first and last of these, 64 rows 239 / 105.
 constexpr int kFewRows = 16;
 
+bool attn_few_rows(int max_new, int G) { return (int64_t)max_new * G <= kFewRows; }
+
 size_t attn_paged_layout(int B, int T, int max_new, int H_kv, int G, int d, void *base, AttnParams *p)
 {
-    if ((int64_t)max_new * G <= kFewRows)
+    if (attn_few_rows(max_new, G))
         return attn_rows_layout(d, base, p);
     return attn_tiles_layout(B, T, H_kv, G, d, base, p);
 }
 
 hipError_t launch_attn_paged(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
-    return (int64_t)p.max_new * p.G <= kFewRows ? launch_attn_rows(p, d, e4m3, stream)
-                                                : launch_attn_tiles(p, d, e4m3, stream);
+    return attn_few_rows(p.max_new, p.G) ? launch_attn_rows(p, d, e4m3, stream) : launch_attn_tiles(p, d, e4m3, stream);
 }
 
 } // namespace gdn

@@ -332,7 +332,7 @@ Sizes sizes_of(int T, int B, int K, int max_new, int H_kv, int G, int d)
     // 128 53.7 / 51.1, 256 71.8 / 72.9, 2048 380 / 403.  Tiles of 64, four a CU, read a group's keys twice as often and
     // leave twice the parts (64 rows 57 -> 59, 3 groups 99 -> 93, before an entry's beginning was counted).  With 256
     // columns the LDS has no room for two.
-    const int tr = d < 256 && rows <= kFewRows ? kFewRows : TR;
+    const int tr = d < 256 && rows <= kSmallTile ? kSmallTile : TR;
     return Sizes{tr, ((size_t)T * G / tr + B) * H_kv, ((size_t)T * G / tr + K) * H_kv,
                  rows >= tr ? tr / 32 : (rows > 32 ? (int)((rows + 31) / 32) : 1)};
 }
@@ -346,6 +346,7 @@ size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int
     const size_t own = (s.own + workgroups) * s.own_blocks, blocks = own + (s.shared + workgroups) * (s.tile_rows / 32);
     const size_t o = round256(blocks * 32 * d * 4), ml = round256(blocks * 32 * 2 * 4),
                  bf = round256((s.own + s.shared + 1) * 8), en = round256((s.own + s.shared) * kSharedEntry * 4);
+    const size_t alone = attn_few_rows(max_new, G) ? attn_paged_layout(B, T, max_new, H_kv, G, d, nullptr, nullptr) : 0;
     if (p) {
         char *at = static_cast<char *>(base);
         p->workgroups = workgroups;
@@ -358,7 +359,8 @@ size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int
         p->entry = reinterpret_cast<int32_t *>(at + o + ml + bf);
         p->count = reinterpret_cast<int32_t *>(at + o + ml + bf + en);
     }
-    return o + ml + bf + en + 256;
+    const size_t all = o + ml + bf + en + 256;
+    return all > alone ? all : alone;
 }
 
 template <int D, bool E4M3>
@@ -366,7 +368,7 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
 {
     const Sizes s = sizes_of(p.T, p.B, p.K, p.max_new, p.H_kv, p.G, D);
     AttnParams q = p;
-    q.block = block_keys(D, p.tile_rows == kFewRows);
+    q.block = block_keys(D, p.tile_rows == kSmallTile);
     // An entry's beginning in blocks' time.  With 0, 1, 2, 3, 5: 64 rows 57, 44, 45, 46, 47 us, 3 groups 99, 90, 86,
     // 87, 91, chunks that are taken together 722, 538, 505, 513, 523; 4 tokens a row (256 columns) 67, 64, 62, 60, 60.
     q.pad = D == 256 ? 3 : 2;
@@ -383,8 +385,26 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     return e;
 }
 
+// Whether the call's sizes alone say that no group will be taken together: every key that the table has room for,
+// read by every tile but one, is less than the plan's rule asks for.
+static bool nothing_to_share(const AttnParams &p, int d)
+{
+    if (p.K == 0 || p.least >= 0)
+        return p.K == 0;
+    const Sizes s = sizes_of(p.T, p.B, p.K, p.max_new, p.H_kv, p.G, d);
+    const double blocks = (double)p.width * (1 << p.page_shift) / block_keys(d, s.tile_rows == kSmallTile);
+    return (double)(s.own - p.H_kv) * blocks < (double)kLeastBlocks * p.workgroups;
+}
+
 hipError_t launch_attn_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
+    // Then rows by themselves in tiles of 16, which need no plan: 8 rows at 16/2 heads of 256 over 500 + 1-40 keys 22.5
+    // -> 15.3 us a call.
+    if (attn_few_rows(p.max_new, p.G) && nothing_to_share(p, d)) {
+        AttnParams q = p;
+        attn_paged_layout(p.B, p.T, p.max_new, p.H_kv, p.G, d, p.part_o, &q); // the workspace's beginning
+        return launch_attn_paged(q, d, e4m3, stream);
+    }
     if (d == 64)
         return e4m3 ? launch_de<64, true>(p, stream) : launch_de<64, false>(p, stream);
     if (d == 128)

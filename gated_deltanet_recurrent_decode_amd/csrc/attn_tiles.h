@@ -7,7 +7,7 @@
 namespace gdn {
 
 // rows of a tile, and of one of a call with few rows a sequence (attn_shared.hip)
-constexpr int TR = 256, kFewRows = 128;
+constexpr int TR = 256, kSmallTile = 128;
 // keys of a block: with 256 columns the queries take half of the LDS
 constexpr int block_keys(int d, bool few = false) { return d == 256 ? 32 : (few ? 64 : 128); }
 constexpr int PT = 1024; // the planning workgroup

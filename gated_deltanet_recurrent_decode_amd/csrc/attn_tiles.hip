@@ -170,13 +170,13 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
     }
 }
 
-constexpr int waves_of(bool few) { return (few ? kFewRows : TR) / 32; }
+constexpr int waves_of(bool few) { return (few ? kSmallTile : TR) / 32; }
 
 // SHARED: of a plan with shared prefixes (attn_shared.hip).  FEW: tiles of 128 rows, two workgroups a CU.
 template <int D, bool E4M3, bool SHARED, bool FEW = false>
 __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnParams p)
 {
-    constexpr int TR = FEW ? kFewRows : gdn::TR;
+    constexpr int TR = FEW ? kSmallTile : gdn::TR;
     constexpr int NW = waves_of(FEW), NT = 64 * NW;
     constexpr int CH = D / 8;                 // chunks of a row
     constexpr int ST = D / 16;                // steps of a score's contraction
@@ -782,7 +782,7 @@ static hipError_t launch_shared(const AttnParams &p, hipStream_t stream)
 // p.tile_rows: 256, or 128 with up to 128 columns
 hipError_t launch_attn_tiles_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
-    const bool few = p.tile_rows == kFewRows;
+    const bool few = p.tile_rows == kSmallTile;
     if (d == 64 && few)
         return e4m3 ? launch_shared<64, true, true>(p, stream) : launch_shared<64, false, true>(p, stream);
     if (d == 64)

@@ -519,7 +519,7 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * with fewer common keys than that are read row by row; -1: those where the joining of
  * the parts would cost more than it saves, by a rule on the lengths.  Every sequence's
  * result is that of attn_paged; its weights are rounded to bf16 at any max_new (o off by
- * 0.0023 of its norm).  A shared length that is longer than what a usable member has
+ * 0.0023 of its norm), but for small calls that attn_paged's own path takes.  A shared length that is longer than what a usable member has
  * before its new tokens counts as that, a negative one as 0; a sequence may be in no
  * group.  A row that reads the common positions through a page outside [1, N) gets
  * NaN in o and lse; the other members' entries for them are not looked at where the

@@ -242,6 +242,22 @@ def test_which_groups_are_read_together():
     check(c, *run(c, least=None, shared=[100, 48]))  # too little to save
 
 
+@pytest.mark.parametrize("d,kind", [(64, "bf16"), (128, "e4m3"), (256, "bf16")])
+def test_as_attn_paged_where_nothing_can_be_shared(d, kind):
+    # short tables, or no groups: single tokens take the path of attn_paged, bit for bit
+    c = Forked([(100, [(1, 3), (2, 40), (1, 0)]), (48, [(1, 9), (1, 5)])], H_q=8, H_kv=2, d=d, page=16, kind=kind, seed=15)
+    out, lse = run(c, least=None)
+    check(c, out, lse)
+    t = c.cuda()
+    paged, plse = torch.empty_like(out), torch.empty_like(lse)
+    ws = torch.empty(gdn.attn_paged_workspace_bytes(c.B, c.T, 2, 8, 2, d), dtype=torch.uint8, device="cuda")
+    gdn.attn_paged(c.q.cuda(), t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"], t["row"], t["cu_seqlens"],
+                   paged, ws, max_new=2, lse=plse, k_scale=t["k_scale"], v_scale=t["v_scale"])
+    nobody = run(c, groups=[0], shared=[])
+    for o, l in ((out, lse), nobody):
+        assert torch.equal(o.view(torch.int16), paged.view(torch.int16)) and torch.equal(l, plse)
+
+
 def test_ranges_that_go_back():
     # the third sequence's tokens lie before the first's: its row by itself, and nobody's parts
     c = Forked([(640, [(2, 5), (2, 9), (2, 3), (2, 4)])], H_q=4, H_kv=2, d=64, page=16, seed=14)
