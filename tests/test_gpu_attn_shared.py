@@ -281,3 +281,25 @@ def test_strided_heads():
     o, _, tol, _ = H.attention(c, 0.125)
     H.check(wide[:, ::2], o, tol, "o")
     assert bool((wide[:, 1::2] == 7).all())
+
+
+def test_two_calls_at_once():
+    # each on its own stream with its own workspace: the bits of one after the other
+    caches = [Forked([(900, [(1, i * 5 % 60) for i in range(20)]), (300, [(1, 8), (1, 2)])], H_q=8, H_kv=2, d=d, page=32,
+                     seed=16 + d) for d in (64, 128)]
+    alone = [run(c) for c in caches]
+    calls = []
+    for c in caches:
+        t, K = c.cuda(), len(c.groups) - 1
+        out = torch.zeros(c.T, c.H_q, c.d, dtype=H.BF, device="cuda")
+        ws = torch.empty(gdn.attn_shared_workspace_bytes(c.B, c.T, K, 1, c.H_q, c.H_kv, c.d), dtype=torch.uint8,
+                         device="cuda")
+        calls.append((c.q.cuda(), t, i32(c.groups), i32(c.shared), out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, t, groups, shared, out, ws, stream in calls:
+            gdn.attn_shared(q, t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"], t["row"], t["cu_seqlens"],
+                            groups, shared, out, ws, max_new=1, least=16, stream=stream)
+    torch.cuda.synchronize()
+    for (o, _), call in zip(alone, calls):
+        assert torch.equal(o.view(torch.int16), call[4].view(torch.int16))

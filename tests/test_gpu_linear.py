@@ -318,3 +318,45 @@ def test_calls_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out[:n], want[:n]) and bool((out[n:] == 0).all()) and torch.equal(so, first)
         assert torch.equal(state[3], want_state[3])
+
+
+def test_slots_past_eight_gib():
+    c = Layer(300, H_k=8, H_v=16, d_k=128, d_v=128, N=3, seed=14)
+    N = 8300  # slots of 1 MiB
+    state = torch.empty(N, 16, 128, 128, device="cuda")
+    state[N - 1] = c.state[1].cuda()
+    q, k, v = c.heads(c.qkv.cuda())
+    g, out = c.g.cuda(), torch.zeros(300, 16, 128, dtype=BF, device="cuda")
+    ws = torch.empty(gdn.lin_attn_prefill_workspace_bytes(1, 299, 8, 16, 128, 128), dtype=torch.uint8, device="cuda")
+    gdn.lin_attn_prefill(q[:299], k[:299], v[:299], g[:299], i32([0, 299]), state, i32([N - 1]), i32([N - 2]), out[:299],
+                         ws, q_scale=c.scale)
+    kept = i32([[N - 3]])
+    gdn.lin_attn_step_tokens(q[None, 299:], k[None, 299:], v[None, 299:], g[None, 299:], state, i32([N - 2]), kept,
+                             out[None, 299:], q_scale=c.scale)
+    torch.cuda.synchronize()
+    o, tol, states = c.reference(0, 300, c.state[1])
+    close(out, o, tol, "out")
+    close(state[N - 2], states[299][0], states[299][1], "the prompt's state")
+    close(state[N - 3], states[300][0], states[300][1], "the state after a token")
+    assert torch.equal(state[N - 1].cpu(), c.state[1])
+
+
+def test_two_prompts_at_once():
+    # each on its own stream with its own workspace: the bits of one after the other
+    layers = [Layer(1500, H_k=2, H_v=4, d_k=64, d_v=64, N=4, seed=15),
+              Layer(900, H_k=2, H_v=2, d_k=128, d_v=128, N=4, seed=16)]
+    alone = [prefill(c, [c.T - 400, 400], [1, 0], [2, 3]) for c in layers]
+    calls = []
+    for c in layers:
+        out = torch.zeros(c.T, c.H_v, c.d_v, dtype=BF, device="cuda")
+        ws = torch.empty(gdn.lin_attn_prefill_workspace_bytes(2, c.T, c.H_k, c.H_v, c.d_k, c.d_v), dtype=torch.uint8,
+                         device="cuda")
+        calls.append(((*c.heads(c.qkv.cuda()), c.g.cuda(), i32([0, c.T - 400, c.T]), c.state.cuda(), i32([1, 0]),
+                       i32([2, 3]), out, ws), c.scale, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for args, scale, stream in calls:
+            gdn.lin_attn_prefill(*args, q_scale=scale, stream=stream)
+    torch.cuda.synchronize()
+    for (out, state), (args, _, _) in zip(alone, calls):
+        assert torch.equal(out, args[8]) and torch.equal(state, args[5])
