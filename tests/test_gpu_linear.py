@@ -328,8 +328,8 @@ def test_slots_past_eight_gib():
     q, k, v = c.heads(c.qkv.cuda())
     g, out = c.g.cuda(), torch.zeros(300, 16, 128, dtype=BF, device="cuda")
     ws = torch.empty(gdn.lin_attn_prefill_workspace_bytes(1, 299, 8, 16, 128, 128), dtype=torch.uint8, device="cuda")
-    gdn.lin_attn_prefill(q[:299], k[:299], v[:299], g[:299], i32([0, 299]), state, i32([N - 1]), i32([N - 2]), out[:299],
-                         ws, q_scale=c.scale)
+    gdn.lin_attn_prefill(q[:299], k[:299], v[:299], g[:299], i32([0, 299]), state, i32([N - 1]), i32([N - 2]),
+                         out[:299], ws, q_scale=c.scale)
     kept = i32([[N - 3]])
     gdn.lin_attn_step_tokens(q[None, 299:], k[None, 299:], v[None, 299:], g[None, 299:], state, i32([N - 2]), kept,
                              out[None, 299:], q_scale=c.scale)
