@@ -13,18 +13,23 @@
 // shorter, the result is the same; only what is read once changes.
 //
 // What bounds it, with few rows: a wave's own chain through a block (scores, maximum, weights, products: 1.05 us for
-// 64 keys, which take the matrix cores 0.4), hidden by one other wave of its SIMD at most, for a tile's registers
-// allow two; an entry's beginning (its record, its page numbers and its first block behind each other, 2.5 us); the
-// plan and the join, 8.5 and 5 to 11 us of a call.  With many rows a sequence: the matrix cores, as in attn_tiles.hip.
-// MI355X, calls back to back: 64 rows at 32/4 heads of 128 over a prefix of 8000 and 50-800 own keys 45 to 47 us (each
-// row by itself 139); 48 rows in 3 groups at 32/8 heads of 128, e4m3, 4000-30000 and 100-1000 86 us (355); 32 rows of 4
-// tokens at 16/4 heads of 256 over 6001 and 10-500 60 us (126); 8 chunks of 100-600 tokens at 32/4 heads of 128 over
-// 12000 492 to 515 us (967 to 924 TFLOP/s), where the rule below takes nothing together.
+// 64 keys, which take the matrix cores 0.4, before weights of two numbers added 0.2), hidden by one other wave of its
+// SIMD at most, for a tile's registers allow two; an entry's beginning (its record, its page numbers and its first
+// block behind each other, 2.5 us); the plan and the join, 8.5 and 5 to 11 us of a call.  With many rows a sequence:
+// the matrix cores, as in attn_tiles.hip.
+// MI355X, calls back to back: 64 rows at 32/4 heads of 128 over a prefix of 8000 and 50-800 own keys 51 to 52 us (each
+// row by itself 139); 48 rows in 3 groups at 32/8 heads of 128, e4m3, 4000-30000 and 100-1000 99 us (355); 32 rows of 4
+// tokens at 16/4 heads of 256 over 6001 and 10-500 67 us (126); 8 chunks of 100-600 tokens at 32/4 heads of 128 over
+// 12000 484 to 515 us (983 to 924 TFLOP/s), where the rule below takes nothing together.
 //
-// Tried, calls: a tile's keys dealt out among its idle waves (the same); the waves' page numbers a block of 64 ahead
-// in a register (the same); own keys by a kernel of 16-row tiles beside the groups' tiles, one more launch (8 rows 30
-// -> 36 us, 64 rows 62 -> 66, 3 groups 123 -> 111, all before the tiles of 128 rows); a block's weight on the line by
-// the waves that have rows (3 groups 86.6 -> 85.1, 64 rows 47.0 -> 49.8, chunks 503 -> 535).
+// Up to 16 rows a sequence keep 15 bits of their weights, as they do in attn_paged: with weights rounded to bf16 o is
+// 0.0023 of its norm off 64 bits in place of 0.0017, and the first three of these calls take 45, 86 and 59 us.
+//
+// Tried, calls, with weights rounded to bf16: a tile's keys dealt out among its idle waves (the same); the waves' page
+// numbers a block of 64 ahead in a register (the same); own keys by a kernel of 16-row tiles beside the groups' tiles,
+// one more launch (8 rows 30 -> 36 us, 64 rows 62 -> 66, 3 groups 123 -> 111, all before the tiles of 128 rows); a
+// block's weight on the line by the waves that have rows (3 groups 86.6 -> 85.1, 64 rows 47.0 -> 49.8, chunks 503 ->
+// 535).
 
 #include "attn_tiles.h"
 #include "gdn_internal.h"
@@ -327,7 +332,8 @@ Sizes sizes_of(int T, int B, int K, int max_new, int H_kv, int G, int d)
 {
     const int64_t rows = (int64_t)max_new * G;
     // Few rows a sequence leave most waves of a 256-row tile idle: then tiles of 128 with blocks of 64 keys, so that a
-    // CU holds two workgroups and one's waits are the other's work (64 rows 57.5 -> 47.5 us, 3 groups 118 -> 89).  By
+    // CU holds two workgroups and one's waits are the other's work (with weights rounded to bf16, as in all figures
+    // here: 64 rows 57.5 -> 47.5 us, 3 groups 118 -> 89).  By
     // the rows of a sequence, 32 of them in 2 groups at 16/2 heads of 128, tiles of 256 / 128: 64 rows 44.1 / 42.7 us,
     // 128 53.7 / 51.1, 256 71.8 / 72.9, 2048 380 / 403.  Tiles of 64, four a CU, read a group's keys twice as often and
     // leave twice the parts (64 rows 57 -> 59, 3 groups 99 -> 93, before an entry's beginning was counted).  With 256
@@ -369,8 +375,9 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     const Sizes s = sizes_of(p.T, p.B, p.K, p.max_new, p.H_kv, p.G, D);
     AttnParams q = p;
     q.block = block_keys(D, p.tile_rows == kSmallTile);
-    // An entry's beginning in blocks' time.  With 0, 1, 2, 3, 5: 64 rows 57, 44, 45, 46, 47 us, 3 groups 99, 90, 86,
-    // 87, 91, chunks that are taken together 722, 538, 505, 513, 523; 4 tokens a row (256 columns) 67, 64, 62, 60, 60.
+    // An entry's beginning in blocks' time.  With 0, 1, 2, 3, 5 (weights rounded to bf16): 64 rows 57, 44, 45, 46, 47
+    // us, 3 groups 99, 90, 86, 87, 91, chunks that are taken together 722, 538, 505, 513, 523; 4 tokens a row (256
+    // columns) 67, 64, 62, 60, 60.
     q.pad = D == 256 ? 3 : 2;
     int own = (int)s.own, shared = (int)s.shared;
     void *plan[] = {&q, &own, &shared}, *args[] = {&q};

@@ -172,8 +172,9 @@ __global__ __launch_bounds__(PT) void attn_plan_kernel(AttnParams p)
 
 constexpr int waves_of(bool few) { return (few ? kSmallTile : TR) / 32; }
 
-// SHARED: of a plan with shared prefixes (attn_shared.hip).  FEW: tiles of 128 rows, two workgroups a CU.
-template <int D, bool E4M3, bool SHARED, bool FEW = false>
+// SHARED: of a plan with shared prefixes (attn_shared.hip).  FEW: tiles of 128 rows, two workgroups a CU.  SPLIT: the
+// products' weights keep 15 bits.
+template <int D, bool E4M3, bool SHARED, bool FEW = false, bool SPLIT = false>
 __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnParams p)
 {
     constexpr int TR = FEW ? kSmallTile : gdn::TR;
@@ -588,9 +589,21 @@ __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnP
                             const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at], scale, off));
                             const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[q >> 1][at + 1], scale, off));
                             l += e0 + e1;
-                            // rounded to bf16 for the matrix cores: off by at most 2^-8 of itself, as o is
-                            // in the end; two numbers for each take half of the products again (above)
-                            pw[q & 1][i >> 1] = pack_bf16(e0, e1);
+                            if constexpr (SPLIT) {
+                                // A weight goes as two bf16 numbers, its upper half and what that leaves (off by at
+                                // most 2^-15 of it together), the second in the place of a score that is done with.
+                                // It is kept above 0 (by 2^-20 of the weight), or an infinity in v that every row
+                                // sees would become a NaN.
+                                const uint32_t y0 = __float_as_uint(e0), y1 = __float_as_uint(e1);
+                                pw[q & 1][i >> 1] = __builtin_amdgcn_perm(y1, y0, 0x07060302u);
+                                sc[q >> 1][8 * (q & 1) + (i >> 1)] = __uint_as_float(
+                                    pack_bf16(fmaf(e0, 1.0f + 0x1p-20f, -__uint_as_float(y0 & 0xffff0000u)),
+                                              fmaf(e1, 1.0f + 0x1p-20f, -__uint_as_float(y1 & 0xffff0000u))));
+                            } else {
+                                // rounded to bf16 for the matrix cores: off by at most 2^-8 of itself, as o is
+                                // in the end; two numbers for each take half of the products again (above)
+                                pw[q & 1][i >> 1] = pack_bf16(e0, e1);
+                            }
                         }
                     };
                     if (D != 256)
@@ -612,6 +625,18 @@ __global__ __launch_bounds__(64 * waves_of(FEW), 2) void attn_tiles_kernel(AttnP
                             f32x16 &o = acc[part * VA + k];
                             o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g & 1][k]),
                                                                         pf, o, 0, 0, 0);
+                        }
+                        if constexpr (SPLIT) {
+                            const f32x16 &x = sc[q >> 1];
+                            const int at = 8 * (q & 1);
+                            const bf16x8 pl =
+                                __builtin_bit_cast(bf16x8, f32x4{x[at], x[at + 1], x[at + 2], x[at + 3]});
+#pragma unroll
+                            for (int k = 0; k < VA; ++k) {
+                                f32x16 &o = acc[part * VA + k];
+                                o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                    __builtin_bit_cast(bf16x8, vf[g & 1][k]), pl, o, 0, 0, 0);
+                            }
                         }
                     }
                 }
@@ -770,28 +795,36 @@ static hipError_t launch_de(const AttnParams &p, hipStream_t stream)
     return e;
 }
 
-template <int D, bool E4M3, bool FEW>
+template <int D, bool E4M3, bool FEW, bool SPLIT>
 static hipError_t launch_shared(const AttnParams &p, hipStream_t stream)
 {
     AttnParams q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, true, FEW>),
+    return hipLaunchKernel(reinterpret_cast<const void *>(&attn_tiles_kernel<D, E4M3, true, FEW, SPLIT>),
                            dim3((unsigned)p.workgroups), dim3(64 * waves_of(FEW)), args, 0, stream);
 }
 
-// p.tile_rows: 256, or 128 with up to 128 columns
+// p.tile_rows: 256, or 128 with up to 128 columns; that few rows have 128
+template <int D, bool E4M3>
+static hipError_t launch_shared_de(const AttnParams &p, hipStream_t stream)
+{
+    const bool split = attn_few_rows(p.max_new, p.G);
+    if constexpr (D == 256) {
+        return split ? launch_shared<D, E4M3, false, true>(p, stream) : launch_shared<D, E4M3, false, false>(p, stream);
+    } else {
+        if (p.tile_rows != kSmallTile)
+            return launch_shared<D, E4M3, false, false>(p, stream);
+        return split ? launch_shared<D, E4M3, true, true>(p, stream) : launch_shared<D, E4M3, true, false>(p, stream);
+    }
+}
+
 hipError_t launch_attn_tiles_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
-    const bool few = p.tile_rows == kSmallTile;
-    if (d == 64 && few)
-        return e4m3 ? launch_shared<64, true, true>(p, stream) : launch_shared<64, false, true>(p, stream);
     if (d == 64)
-        return e4m3 ? launch_shared<64, true, false>(p, stream) : launch_shared<64, false, false>(p, stream);
-    if (d == 128 && few)
-        return e4m3 ? launch_shared<128, true, true>(p, stream) : launch_shared<128, false, true>(p, stream);
+        return e4m3 ? launch_shared_de<64, true>(p, stream) : launch_shared_de<64, false>(p, stream);
     if (d == 128)
-        return e4m3 ? launch_shared<128, true, false>(p, stream) : launch_shared<128, false, false>(p, stream);
-    return e4m3 ? launch_shared<256, true, false>(p, stream) : launch_shared<256, false, false>(p, stream);
+        return e4m3 ? launch_shared_de<128, true>(p, stream) : launch_shared_de<128, false>(p, stream);
+    return e4m3 ? launch_shared_de<256, true>(p, stream) : launch_shared_de<256, false>(p, stream);
 }
 
 hipError_t launch_attn_tiles(const AttnParams &p, int d, bool e4m3, hipStream_t stream)

@@ -518,12 +518,12 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * its first usable sequence (the rest of each row through its own).  least >= 0: groups
  * with fewer common keys than that are read row by row; -1: those where the joining of
  * the parts would cost more than it saves, by a rule on the lengths.  Every sequence's
- * result is that of attn_paged; its weights are rounded to bf16 at any max_new (o off by
- * 0.0023 of its norm), but for small calls that attn_paged's own path takes.  A shared length that is longer than what a usable member has
- * before its new tokens counts as that, a negative one as 0; a sequence may be in no
- * group.  A row that reads the common positions through a page outside [1, N) gets
- * NaN in o and lse; the other members' entries for them are not looked at where the
- * group is read together.
+ * result is that of attn_paged within rounding, with as many bits: weights keep 15
+ * where max_new * H_q / H_kv <= 16 and are rounded to bf16 beyond.  A shared length that
+ * is longer than what a usable member has before its new tokens counts as that, a
+ * negative one as 0; a sequence may be in no group.  A row that reads the common
+ * positions through a page outside [1, N) gets NaN in o and lse; the other members'
+ * entries for them are not looked at where the group is read together.
  * cu_groups [groups + 1] and shared_len [groups] int32 on the device (NULL with groups
  * 0); 0 <= groups <= 1024.  Preconditions, not checked: cu_groups is non-decreasing in
  * [0, B]; the common cells agree.  workspace: attn_shared_workspace_bytes(dims, groups)
