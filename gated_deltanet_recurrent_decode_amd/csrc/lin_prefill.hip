@@ -659,26 +659,40 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
     // and its state's way through memory cost about as much as kFixed tokens: segments half as long take 77, 146 and
     // 223 us of the three cases above, twice as long 78, 123 and 335, these 76, 126 and 205.  kMost: where no rounds
     // fit (thousands of sequences), and none longer, so that one long prompt among them does not outlast the rest.
-    constexpr int64_t kFixed = 160, kMost = 2048;
+    constexpr int64_t kFixed = 160, kMost = 2048, kFewest = 4 * C;
     const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
     const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);
-    int64_t segment = 0, least = 0;
+    int64_t segment = 0, least = 0, most = 0;
     for (int64_t rounds = 1; rounds <= 8; ++rounds) {
-        const int64_t most = rounds * slots / groups; // segments: (T + B (L - 1)) / L of them at most
-        if (most < B || T < B)
+        most = rounds * slots / groups; // segments: (T + B (L - 1)) / L of them at most
+        if (most < B)
             continue;
-        int64_t L = (T - B) / (most - B + 1) + 1;
-        L = ((L < 4 * C ? 4 * C : L) + C - 1) / C * C;
-        if (least == 0 || rounds * (L + kFixed) < least) {
-            least = rounds * (L + kFixed);
-            segment = L;
+        if (T >= B) {
+            int64_t L = (T - B) / (most - B + 1) + 1;
+            L = ((L < kFewest ? kFewest : L) + C - 1) / C * C;
+            if (least == 0 || rounds * (L + kFixed) < least) {
+                least = rounds * (L + kFixed);
+                segment = L;
+            }
         }
+        // Up to whole segments and rounds the cost is most (T / (most - B) + kFixed), least where this becomes equal.
+        if ((most - B) * (most - B) * kFixed >= (int64_t)B * T)
+            break;
     }
     if (segment == 0 || segment > kMost)
         segment = kMost;
     const int64_t segments = T / segment + B;
-    const size_t entry = T > segment ? round256((size_t)segments * H_v * d_k * d_v * 4) : 0;
-    const size_t decay = T > segment ? round256((size_t)segments * H_v * 4) : 0;
+    // Fewer sequences or tokens may have shorter segments, and more of them.  So that one workspace serves all calls up
+    // to the largest, it has room for what no such call passes: with T - B < L (most - B + 1) places T / L + B are at
+    // most most + ceil(B / L), and `most` is the last that was looked at, which only grows with B and T.
+    int64_t room = 0;
+    if (T > kFewest) {
+        room = most + (B + kFewest - 1) / kFewest;
+        room = T / kFewest + B < room ? T / kFewest + B : room;
+        if (T > kMost && T / kMost + B > room)
+            room = T / kMost + B;
+    }
+    const size_t entry = round256((size_t)room * H_v * d_k * d_v * 4), decay = round256((size_t)room * H_v * 4);
     if (p) {
         p->segment = (int)segment;
         p->segments = (int)segments;

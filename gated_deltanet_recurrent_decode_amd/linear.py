@@ -134,7 +134,8 @@ def lin_attn_step_tokens(q, k, v, g, state, read_slot, token_slots, out, *, q_sc
 
 
 def lin_attn_prefill_workspace_bytes(B: int, T: int, H_k: int, H_v: int, d_k: int, d_v: int) -> int:
-    """The workspace lin_attn_prefill needs for B sequences of T tokens in all, in bytes, on the current GPU."""
+    """The workspace lin_attn_prefill needs for up to B sequences of up to T tokens in all, in bytes, on the current
+    GPU."""
     n = lib().lin_attn_prefill_workspace_bytes(_DIMS.pack(B, T, H_k, H_v, d_k, d_v, 1, 0))
     if n == 0:
         raise GdnError("lin_attn_prefill_workspace_bytes", 2)

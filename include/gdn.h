@@ -693,7 +693,8 @@ gdn_status lin_attn_step_tokens(const gdn_lin_dims *dims, const gdn_heads *q, co
  * another's read slot.
  * workspace: lin_attn_prefill_workspace_bytes(dims) bytes of device memory, 256-byte
  * aligned, contents of no matter before and after; calls that share one must be
- * stream-ordered.
+ * stream-ordered.  One that is large enough for some B and T serves calls with fewer
+ * sequences and tokens of the same heads.
  * B = 0 returns GDN_OK at once; with T = 0 the arrays of tokens may be NULL.  Statuses
  * as lin_attn_step; GDN_ERR_SHAPE also for a workspace too small.
  */
@@ -702,8 +703,9 @@ gdn_status lin_attn_prefill(const gdn_lin_dims *dims, const gdn_heads *q, const 
                             const int32_t *write_slot, const gdn_heads *out, float q_scale, void *workspace,
                             size_t workspace_bytes, hipStream_t stream);
 
-/* The workspace lin_attn_prefill needs for dims (B, T, H_v, d_k, d_v); 0 when dims is
- * NULL or its sizes are unusable. */
+/* The workspace lin_attn_prefill needs for dims (B, T, H_k, H_v, d_k, d_v; it never falls
+ * as B or T grows); 0 when dims is NULL or one of its sizes, N and per_token among them,
+ * is unusable. */
 size_t lin_attn_prefill_workspace_bytes(const gdn_lin_dims *dims);
 
 /* Static text for a status code (host only). */
