@@ -31,6 +31,8 @@
 // block's weight on the line by the waves that have rows (3 groups 86.6 -> 85.1, 64 rows 47.0 -> 49.8, chunks 503 ->
 // 535).
 
+#include <algorithm>
+
 #include "attn_tiles.h"
 #include "gdn_internal.h"
 
@@ -352,7 +354,6 @@ size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int
     const size_t own = (s.own + workgroups) * s.own_blocks, blocks = own + (s.shared + workgroups) * (s.tile_rows / 32);
     const size_t o = round256(blocks * 32 * d * 4), ml = round256(blocks * 32 * 2 * 4),
                  bf = round256((s.own + s.shared + 1) * 8), en = round256((s.own + s.shared) * kSharedEntry * 4);
-    const size_t alone = attn_few_rows(max_new, G) ? attn_paged_layout(B, T, max_new, H_kv, G, d, nullptr, nullptr) : 0;
     if (p) {
         char *at = static_cast<char *>(base);
         p->workgroups = workgroups;
@@ -365,8 +366,12 @@ size_t attn_shared_layout(int B, int T, int K, int max_new, int H_kv, int G, int
         p->entry = reinterpret_cast<int32_t *>(at + o + ml + bf);
         p->count = reinterpret_cast<int32_t *>(at + o + ml + bf + en);
     }
-    const size_t all = o + ml + bf + en + 256;
-    return all > alone ? all : alone;
+    // A workspace for some max_new serves calls with less, whose tiles may be smaller and more, or attn_paged's.
+    size_t all = o + ml + bf + en + 256;
+    const int fewer = kSmallTile / G;
+    if (fewer > 0 && s.tile_rows != kSmallTile && d < 256 && max_new > fewer)
+        all = std::max(all, attn_shared_layout(B, T, K, fewer, H_kv, G, d, nullptr, nullptr));
+    return attn_few_rows(1, G) ? std::max(all, attn_paged_layout(B, T, 1, H_kv, G, d, nullptr, nullptr)) : all;
 }
 
 template <int D, bool E4M3>

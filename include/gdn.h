@@ -527,8 +527,9 @@ size_t attn_paged_workspace_bytes(const gdn_attn_dims *dims);
  * cu_groups [groups + 1] and shared_len [groups] int32 on the device (NULL with groups
  * 0); 0 <= groups <= 1024.  Preconditions, not checked: cu_groups is non-decreasing in
  * [0, B]; the common cells agree.  workspace: attn_shared_workspace_bytes(dims, groups)
- * bytes.  The rest, and statuses, as attn_paged (GDN_ERR_SHAPE also for groups, and where
- * (T H_q / H_kv / 128 + B) H_kv is 2^24 or more).
+ * bytes; one that is large enough for some B, T, max_new and groups serves calls with
+ * less of each.  The rest, and statuses, as attn_paged (GDN_ERR_SHAPE also for groups, and
+ * where (T H_q / H_kv / 128 + B) H_kv is 2^24 or more).
  */
 gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
                        const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
@@ -536,7 +537,11 @@ gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_
                        hipStream_t stream);
 
 /* The workspace attn_shared needs for dims (B, T, max_new, H_q, H_kv, d) and groups; 0
- * when dims is NULL or a size is unusable. */
+ * when dims is NULL or a size is unusable.  It grows with the batch, where attn_paged's
+ * parts do not: each sequence and kv head has room for a part of max_new H_q / H_kv rows
+ * of d floats, rounded up to 32 (256 at most), and all tokens for two copies of their
+ * rows' parts more.  1024 single tokens at 32/8 heads of 128 take 205 MB, 16384 tokens of
+ * chunks at 64/8 heads of 128 1.2 GB. */
 size_t attn_shared_workspace_bytes(const gdn_attn_dims *dims, int32_t groups);
 
 /*
