@@ -57,8 +57,10 @@ __device__ __forceinline__ float log2_decay(float g)
     return x < kLeast ? kLeast : x; // a NaN stays
 }
 
-// The logarithm range that a state and a chunk's weights may share one scale in: 2^-64 .. 2^64.
-constexpr float kRange = 64.0f;
+// The logarithm range that a state and a chunk's weights may share one scale in: 2^-32 .. 2^32.  What fp32 holds of v,
+// of a state and of a read-out's sums ends that much earlier.  Calls with 2^16, 2^32 and 2^64, us: a long prompt 80.2,
+// 79.9, 79.1, ragged ones 126.4, 126.0, 125.8, grouped heads 204.6, 203.5, 201.5.
+constexpr float kRange = 32.0f;
 
 // 2^x of a 64-bit logarithm: its fraction keeps all bits of fp32.
 __device__ __forceinline__ float exp2_of(double x)

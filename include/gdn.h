@@ -685,8 +685,8 @@ gdn_status lin_attn_step_tokens(const gdn_lin_dims *dims, const gdn_heads *q, co
  * matrix cores, decayed values go into the state as three bf16 numbers, with all their
  * bits; the state and the weights that make a read-out go as two, off by at most
  * 2^-15 of themselves, before o is rounded once, to bf16.  Within a call a state is held
- * at up to 2^64 times its value: entries of v or of the state of 2^63 (9e18) and more
- * may come out as infinities.
+ * at up to 2^32 times its value: where an entry of v, of a state or of k v^T, or a sum
+ * over d_k of |q| |S|, is 2^95 (4e28) or more, infinities may come out.
  * Results match lin_attn_step within rounding, not bit for bit, and the same call gives
  * the same bits again.  An infinity or NaN in a token shows from that token on, as an
  * infinity or NaN, and nowhere before.
