@@ -548,8 +548,8 @@ def traffic_probe(state, read_slot, write_slot, sink, *, traffic: str = "copy", 
 
 from . import attention as _attention  # noqa: E402  (it takes this module's helpers)
 from .attention import (attn_paged, attn_paged_workspace_bytes, attn_prologue, attn_shared,  # noqa: E402
-                        attn_shared_workspace_bytes, kv_page_compact, kv_page_copy, kv_page_fork, kv_page_free, kv_page_reserve, kv_page_workspace_bytes,
-                        rope_freqs)
+                        attn_shared_workspace_bytes, kv_page_compact, kv_page_copy, kv_page_fork, kv_page_free,
+                        kv_page_reserve, kv_page_workspace_bytes, rope_freqs)
 
 EXPORTS += _attention.EXPORTS
 

@@ -326,7 +326,8 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, out, wo
 
 
 def attn_shared_workspace_bytes(B: int, T: int, K: int, max_new: int, H_q: int, H_kv: int, d: int) -> int:
-    """The workspace attn_shared needs for K groups (see include/gdn.h), in bytes, on the current GPU."""
+    """The workspace attn_shared needs for up to B sequences, T tokens, K groups and max_new tokens of a sequence (see
+    include/gdn.h), in bytes, on the current GPU."""
     n = lib().attn_shared_workspace_bytes(_DIMS.pack(B, T, 1, H_q, H_kv, d, 1, 16, 1, max_new, 0, 0), K)
     if n == 0:
         raise GdnError("attn_shared_workspace_bytes", 2)
@@ -334,13 +335,15 @@ def attn_shared_workspace_bytes(B: int, T: int, K: int, max_new: int, H_q: int, 
 
 
 def attn_shared(q, k_pages, v_pages, page_table, kv_len, row, cu_seqlens, cu_groups, shared_len, out, workspace, *,
-                max_new: int, scale: float | None = None, window: int = 0, least: int | None = None, lse=None, k_scale=None,
-                v_scale=None, stream=None) -> None:
+                max_new: int, scale: float | None = None, window: int = 0, least: int | None = None, lse=None,
+                k_scale=None, v_scale=None, stream=None) -> None:
     """attn_paged for sequences that share prefixes, which are read once a group (see ``attn_shared`` in
     include/gdn.h).
 
     cu_groups [K+1] and shared_len [K] int32: sequences cu_groups[g] .. cu_groups[g+1]-1 have the same first
-    shared_len[g] positions, read together from `least` keys on (None: where it pays); workspace a uint8 tensor of attn_shared_workspace_bytes; the rest as attn_paged."""
+    shared_len[g] positions, read together from `least` keys on (None: by a rule on the lengths); workspace a uint8
+    tensor of attn_shared_workspace_bytes, which grows with the batch; the rest as attn_paged.  Where little is shared
+    attn_paged is the faster call."""
     torch = _torch()
     bf, i32 = torch.bfloat16, torch.int32
     N, H_kv, page, d, R, width, kind = _cache_layout(k_pages, v_pages, page_table, kv_len, k_scale, v_scale)

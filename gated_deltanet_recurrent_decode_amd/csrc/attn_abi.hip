@@ -64,7 +64,6 @@ gdn_status attn_setup(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_k
                       gdn::AttnParams &p, bool *run)
 {
     *run = false;
-
     if (!dims)
         return GDN_ERR_NULL;
     const gdn_attn_dims d = *dims;
@@ -254,8 +253,8 @@ size_t attn_shared_workspace_bytes(const gdn_attn_dims *dims, int32_t groups)
 
 gdn_status attn_shared(const gdn_attn_dims *dims, const gdn_heads *q, const gdn_kv_cache *cache, const int32_t *row,
                        const int32_t *cu_seqlens, const int32_t *cu_groups, const int32_t *shared_len, int32_t groups,
-                       int32_t least, const gdn_heads *out, float *lse, float scale, void *workspace, size_t workspace_bytes,
-                       hipStream_t stream)
+                       int32_t least, const gdn_heads *out, float *lse, float scale, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream)
 {
     gdn::AttnParams p{};
     bool run;

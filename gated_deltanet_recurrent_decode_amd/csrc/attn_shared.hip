@@ -17,10 +17,13 @@
 // SIMD at most, for a tile's registers allow two; an entry's beginning (its record, its page numbers and its first
 // block behind each other, 2.5 us); the plan and the join, 8.5 and 5 to 11 us of a call.  With many rows a sequence:
 // the matrix cores, as in attn_tiles.hip.
-// MI355X, calls back to back: 64 rows at 32/4 heads of 128 over a prefix of 8000 and 50-800 own keys 51 to 52 us (each
-// row by itself 139); 48 rows in 3 groups at 32/8 heads of 128, e4m3, 4000-30000 and 100-1000 99 us (355); 32 rows of 4
-// tokens at 16/4 heads of 256 over 6001 and 10-500 67 us (126); 8 chunks of 100-600 tokens at 32/4 heads of 128 over
-// 12000 484 to 515 us (983 to 924 TFLOP/s), where the rule below takes nothing together.
+// MI355X, calls back to back, and attn_paged's of the same rows: 64 rows at 32/4 heads of 128 over a prefix of 8000 and
+// 50-800 own keys 51 to 52 us (attn_paged 88); 48 rows in 3 groups at 32/8 heads of 128, e4m3, 4000-30000 and 100-1000
+// 99 us (270); 32 rows of 4 tokens at 16/4 heads of 256 over 6001 and 10-500 67 us (117); 8 chunks of 100-600 tokens at
+// 32/4 heads of 128 over 12000 484 to 515 us (481; 983 to 924 TFLOP/s), where the rule below takes nothing together.
+// The plan, the join and tiles that few rows leave idle cost more than sharing saves where little is shared: at 16/2
+// heads of 128 with 10-500 own keys 8 rows over 4000 28.5 us (20.0), 64 over 1024 30.4 (23.2), 64 in 16 groups over
+// 2048 33.4 (30.1), 64 in 32 groups over 8192 74.6 (77.3).
 //
 // Up to 16 rows a sequence keep 15 bits of their weights, as they do in attn_paged: with weights rounded to bf16 o is
 // 0.0023 of its norm off 64 bits in place of 0.0017, and the first three of these calls take 45, 86 and 59 us.
@@ -43,13 +46,13 @@ namespace {
 // Which groups are taken together where the call does not say.  Members with tiles of their own read a key once a
 // tile; together they are fewer tiles.  For that the rows' second parts have to be written and joined, about 512
 // keys' time for a tile of a member, and the group's own tiles begun, 1024 each.  16/2 heads of 128, 512 rows with
-// 10-2000 own keys, each row by itself / together, us: 256 groups of about 2 at a prefix of 1024 182 / 180, of 2048
-// 244 / 224, of 8192 622 / 491; 64 groups of about 8 at 512 139 / 148, of 1024 155 / 153, of 4096 313 / 191.  Chunks
+// 10-2000 own keys, by tiles of their own / together, us: 256 groups of about 2 at a prefix of 1024 184 / 183, of 2048
+// 248 / 227, of 8192 653 / 502; 64 groups of about 8 at 512 142 / 152, of 1024 155 / 155, of 4096 317 / 197.  Chunks
 // of 100-600 tokens fill their own tiles: 499 / 509 with 12000 common keys.
 constexpr int kPerMember = 512, kPerTile = 1024;
 // And the call as a whole saves at least so many blocks a workgroup: below, a step of few rows is bound by how long a
-// workgroup takes at all (64 rows in 16 groups at 1024, 3 blocks: 33.5 / 33.3; at 2048, 6: 41.6 / 37.6; 8 rows of one
-// group at 4096, 2: 27.9 / 28.7; 64 rows of one at 1024, 4: 26.8 / 27.9).
+// workgroup takes at all (the same with 64 rows in 16 groups at 1024, 3 blocks: 35.5 / 36.0; at 2048, 6: 43.1 / 40.1;
+// 64 rows of one at 1024, 4: 36.7 / 36.8; 16 rows in 2 groups at 4096, 4: 31.7 / 32.7).
 constexpr int kLeastBlocks = 5;
 
 // The last x of n with first[x] <= v, the first at least.
@@ -410,8 +413,9 @@ static bool nothing_to_share(const AttnParams &p, int d)
 
 hipError_t launch_attn_shared(const AttnParams &p, int d, bool e4m3, hipStream_t stream)
 {
-    // Then rows by themselves in tiles of 16, which need no plan: 8 rows at 16/2 heads of 256 over 500 + 1-40 keys 22.5
-    // -> 15.3 us a call.
+    // Then rows by themselves in tiles of 16, which need no plan: 8 rows at 16/2 heads of 256 over 500 + 1-40 keys 15.1
+    // us a call, and 23.2 with a table of 4096 positions or more, where the rule would have room to hold: only the
+    // device knows the lengths.
     if (attn_few_rows(p.max_new, p.G) && nothing_to_share(p, d)) {
         AttnParams q = p;
         attn_paged_layout(p.B, p.T, p.max_new, p.H_kv, p.G, d, p.part_o, &q); // the workspace's beginning

@@ -20,8 +20,9 @@
 //
 // What bounds it: memory, with what the segments add to it.  8191 tokens at 16 heads of 128 x 128 have to move 135 MB
 // (26 us at a large copy's 5.2 TB/s) and move 334, k and v twice and the segments' states four times; own parts 25 us,
-// carry 12, walk 40, calls back to back 74 to 76; without any of its products the walk is 10% faster.  16 prompts of
-// 100-1500 tokens 124 us, 4 of 5000-9000 with four value heads of 64 columns a key head 202 to 204, one of 77 10.4.
+// carry 12, walk 40 to 43, calls back to back 74 to 80; without any of its products the walk is 10% faster.  16 prompts
+// of 100-1500 tokens 124 to 126 us, 4 of 5000-9000 with four value heads of 64 columns a key head 202 to 205, one of 77
+// 10.5.
 //
 // Scores and scales are dealt out among a head's waves (each forming all for itself: 89 -> 81 us, the long
 // prompt's call); two barriers a chunk with 48 KiB of LDS less (81 -> 76).  Two value heads of a key head in one
@@ -660,7 +661,11 @@ size_t lin_prefill_layout(int B, int T, int H_k, int H_v, int d_k, int d_v, void
     // at once, sequences' last ones counted as whole, with the rounds that cost least.  A workgroup's start and end
     // and its state's way through memory cost about as much as kFixed tokens: segments half as long take 77, 146 and
     // 223 us of the three cases above, twice as long 78, 123 and 335, these 76, 126 and 205.  kMost: where no rounds
-    // fit (thousands of sequences), and none longer, so that one long prompt among them does not outlast the rest.
+    // fit, which is with more sequences than 8 slots / groups (64 at 64 heads of 128 x 128) and close to that, and none
+    // longer, so that one long prompt among many does not outlast the rest.  With 512, 1024, 2048, 4096, 8192, us: 64
+    // heads of 128 x 128, one prompt of 8000 among 79 of 100 1074, 1138, 1117, 1085, 909, four of 4000 among 76 of 100
+    // 1239, 1568, 1848, 1552, 1562, 80 of 300-500 531, 533, 523, 529, 535; 16 heads, one of 8000 among 299 of 50 425,
+    // 424, 428, 501, 621.  512 has four times the segments of long prompts in the workspace.
     constexpr int64_t kFixed = 160, kMost = 2048, kFewest = 4 * C;
     const bool pair = d_v == 64 && H_v / H_k % 2 == 0;
     const int64_t groups = pair ? H_v / 2 : H_v, slots = (int64_t)device_cus() * walks_a_cu(d_k, d_v, pair);
